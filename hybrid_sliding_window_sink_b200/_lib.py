@@ -29,6 +29,8 @@ EXPORTS = ("mimo_attn_prefill", "mimo_attn_decode", "mimo_attn_sparse", "mimo_at
            "mimo_attn_decode_mq", "mimo_attn_decode_mq_workspace_size", "mimo_attn_workspace_size",
            "mimo_attn_decode_fp8", "mimo_attn_sparse_fp8", "mimo_attn_prefill_chunk",
            "mimo_attn_cache_append", "mimo_attn_select_tokens", "mimo_attn_select_workspace_size",
+           "mimo_attn_decode_paged", "mimo_attn_decode_paged_fp8", "mimo_attn_decode_paged_workspace_size",
+           "mimo_attn_cache_append_paged", "mimo_attn_cache_append_paged_fp8", "mimo_attn_verify_drafts",
            "mimo_attn_check_indices", "mimo_attn_last_device_error", "mimo_attn_device_status",
            "mimo_status_string", "mimo_attn_version")
 
@@ -46,6 +48,11 @@ class MimoShape(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int), ("seqlen", ctypes.c_int), ("n_q_heads", ctypes.c_int),
                 ("n_kv_heads", ctypes.c_int), ("head_dim_qk", ctypes.c_int),
                 ("head_dim_v", ctypes.c_int), ("softmax_scale", ctypes.c_float)]
+
+
+class MimoPages(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("page_stride_tokens", ctypes.c_longlong)]
 
 
 _LIB = None
@@ -82,6 +89,14 @@ def load(path):
     L.mimo_attn_select_workspace_size.restype = SZ
     L.mimo_attn_decode_fp8.argtypes = [SP, P, P, P, P, P, I, I, LL, P, P, P, P, P, SZ, P]
     L.mimo_attn_sparse_fp8.argtypes = [SP, P, P, P, P, P, I, LL, P, I, P, I, P, P, P, P, SZ, P]
+    PP = ctypes.POINTER(MimoPages)
+    L.mimo_attn_decode_paged.argtypes = [SP, P, P, P, PP, P, I, I, P, P, P, P, SZ, P]
+    L.mimo_attn_decode_paged_fp8.argtypes = [SP, P, P, P, P, P, PP, P, I, I, P, P, P, P, SZ, P]
+    L.mimo_attn_decode_paged_workspace_size.argtypes = [SP, PP, I, I]
+    L.mimo_attn_decode_paged_workspace_size.restype = SZ
+    L.mimo_attn_cache_append_paged.argtypes = [SP, P, P, P, P, F, I, PP, P, P, P]
+    L.mimo_attn_cache_append_paged_fp8.argtypes = [SP, P, P, P, P, F, I, PP, P, P, P, P, P]
+    L.mimo_attn_verify_drafts.argtypes = [I, I, I, I, P, P, P, P, P, P, P, P]
     L.mimo_attn_workspace_size.argtypes = [SP, I, I, I, I, I]
     L.mimo_attn_workspace_size.restype = SZ
     L.mimo_attn_check_indices.argtypes = [SP, P, P, I, I, I, P, P]
@@ -101,6 +116,10 @@ def load(path):
 
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
@@ -405,6 +424,237 @@ def sparse(q, k_cache, v_cache, lengths, sel_idx, sink=None, *, recent=128, capa
                                 _ptr(out), _ptr(lse), _ptr(ws), nbytes, _stream(stream))
     _check("mimo_attn_sparse", st)
     return out, lse
+
+
+class _On:
+    """Makes the tensors' device current and yields the raw stream to launch on: the given
+    stream (which must belong to that device), or the device's current one. Scratch and outputs
+    allocated inside belong to that stream."""
+
+    __slots__ = ("ctx", "stream")
+
+    def __init__(self, device, stream):
+        self.ctx = None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream of {stream.device} for tensors on {device}")
+            self.ctx = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+        self.stream = stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream()
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _need_at(t, name, dtype, shape, device, contiguous=True):
+    """t is a tensor of that dtype, shape (None: any size) and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    have = t.shape
+    if len(have) != len(shape) or any(n is not None and n != h for n, h in zip(shape, have)):
+        raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, got {tuple(have)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _cuda_device(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _pages(k, v, table, scales=()):
+    """mimo_pages of the pools k [num_pages, page_size, Hkv, 192], v [.., 128] and the scales
+    [num_pages, page_size, Hkv]: each contiguous within a page, with the same distance between
+    pages, in whole tokens."""
+    n, page, hkv = k.shape[:3]
+    if n < 1 or page < 1 or hkv < 1:
+        raise ValueError("the pool holds no page")
+    stride = None
+    for name, t in (("k_pages", k), ("v_pages", v), *scales):
+        row = hkv * t.shape[3] if t.dim() == 4 else hkv
+        inner = (row, t.shape[3], 1) if t.dim() == 4 else (row, 1)
+        if any(s != w and d > 1 for s, w, d in zip(t.stride()[1:], inner, t.shape[1:])):
+            raise ValueError(f"{name} must be contiguous within a page")
+        step = t.stride(0) if n > 1 else page * row
+        if step % row or step < page * row:
+            raise ValueError(f"{name}: pages must not overlap and must lie whole tokens apart")
+        if stride is not None and step // row != stride:
+            raise ValueError("K, V and scale pools must have the same distance between pages")
+        stride = step // row
+    return MimoPages(table.data_ptr(), table.shape[1], n, page, stride)
+
+
+def _decode_paged(q, k, v, scales, table, lengths, sink, window, n_first, softmax_scale, out, lse, want_lse,
+                  workspace, stream):
+    dev = _cuda_device(q, "q")
+    fp8 = scales is not None
+    _need_at(q, "q", torch.bfloat16, (None, None, 192), dev)
+    B, hq = q.shape[:2]
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    _need_at(k, "k_pages", dt, (None, None, None, 192), dev, contiguous=False)
+    n, page, hkv = k.shape[:3]
+    _need_at(v, "v_pages", dt, (n, page, hkv, 128), dev, contiguous=False)
+    _need_at(table, "block_table", torch.int32, (B, None), dev)
+    _need_at(lengths, "lengths", torch.int32, (B,), dev)
+    named = ()
+    if fp8:
+        named = (("k_scale", scales[0]), ("v_scale", scales[1]))
+        for name, t in named:
+            _need_at(t, name, torch.float32, (n, page, hkv), dev, contiguous=False)
+    if sink is not None:
+        _need_at(sink, "sink", torch.float32, (hq,), dev)
+    if out is not None:
+        _need_at(out, "out", torch.bfloat16, (B, hq, 128), dev)
+    if lse is not None:
+        _need_at(lse, "lse", torch.float32, (B, hq), dev)
+    pages = _pages(k, v, table, named)
+    shape = MimoShape(B, 1, hq, hkv, 192, 128, float(softmax_scale))
+    L = lib()
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty(B, hq, 128, dtype=torch.bfloat16, device=dev)
+        if lse is None and want_lse:
+            lse = torch.empty(B, hq, dtype=torch.float32, device=dev)
+        nbytes = L.mimo_attn_decode_paged_workspace_size(shape, pages, int(window), int(n_first))
+        if workspace is not None:
+            _cuda_device(workspace, "workspace")
+            if workspace.device != dev or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be contiguous and on {dev}")
+        ws = _workspace(workspace, nbytes, dev)
+        tail = (_addr(sink), out.data_ptr(), _addr(lse), _addr(ws), nbytes, st)
+        if fp8:
+            rc = L.mimo_attn_decode_paged_fp8(shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), scales[0].data_ptr(),
+                                              scales[1].data_ptr(), pages, lengths.data_ptr(), int(window),
+                                              int(n_first), *tail)
+        else:
+            rc = L.mimo_attn_decode_paged(shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), pages,
+                                          lengths.data_ptr(), int(window), int(n_first), *tail)
+    _check("mimo_attn_decode_paged_fp8" if fp8 else "mimo_attn_decode_paged", rc)
+    return out, lse
+
+
+def decode_paged(q, k_pages, v_pages, block_table, lengths, sink=None, *, window=0, n_first=0, softmax_scale=0.0,
+                 out=None, lse=None, want_lse=True, workspace=None, stream=None):
+    """mimo_attn_decode_paged. q [B,Hq,192]; k_pages [N,page,Hkv,192], v_pages [N,page,Hkv,128] bf16
+    (rotated K; pages may lie further apart than their size); block_table [B,max_pages] and lengths
+    [B] int32. The query sees the last ``window`` tokens and the first ``n_first`` ones (window <= 0:
+    everything). Returns (out [B,Hq,128] bf16, lse [B,Hq] fp32 or None)."""
+    return _decode_paged(q, k_pages, v_pages, None, block_table, lengths, sink, window, n_first, softmax_scale, out,
+                         lse, want_lse, workspace, stream)
+
+
+def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, lengths, sink=None, *, window=0, n_first=0,
+                     softmax_scale=0.0, out=None, lse=None, want_lse=True, workspace=None, stream=None):
+    """mimo_attn_decode_paged_fp8: decode_paged() over E4M3 pages (uint8) with k_scale / v_scale
+    [N,page,Hkv] fp32."""
+    return _decode_paged(q, k_pages, v_pages, (k_scale, v_scale), block_table, lengths, sink, window, n_first,
+                         softmax_scale, out, lse, want_lse, workspace, stream)
+
+
+def decode_paged_workspace_size(batch, hq, hkv, *, max_pages, page_size, window=0, n_first=0):
+    """Bytes of workspace the paged decodes need on the current device."""
+    pages = MimoPages(None, int(max_pages), 1, int(page_size), int(page_size))
+    return int(lib().mimo_attn_decode_paged_workspace_size(make_shape(batch, 1, hq, hkv), pages, int(window),
+                                                           int(n_first)))
+
+
+def _append_paged(k_new, v_new, k, v, scales, table, positions, n_new, rope_theta, rot_dims, stream):
+    dev = _cuda_device(k_new, "k_new")
+    fp8 = scales is not None
+    _need_at(k_new, "k_new", torch.bfloat16, (None, None, None, 192), dev)
+    B, n, hkv = k_new.shape[:3]
+    _need_at(v_new, "v_new", torch.bfloat16, (B, n, hkv, 128), dev)
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    _need_at(k, "k_pages", dt, (None, None, hkv, 192), dev, contiguous=False)
+    N, page = k.shape[:2]
+    _need_at(v, "v_pages", dt, (N, page, hkv, 128), dev, contiguous=False)
+    _need_at(table, "block_table", torch.int32, (B, None), dev)
+    _need_at(positions, "positions", torch.int32, (B,), dev)
+    if n_new is not None:
+        _need_at(n_new, "n_new", torch.int32, (B,), dev)
+    named = ()
+    if fp8:
+        named = (("k_scale", scales[0]), ("v_scale", scales[1]))
+        for name, t in named:
+            _need_at(t, name, torch.float32, (N, page, hkv), dev, contiguous=False)
+    pages = _pages(k, v, table, named)
+    shape = MimoShape(B, n, hkv, hkv, 192, 128, 0.0)
+    with _On(dev, stream) as st:
+        head = (shape, k_new.data_ptr(), v_new.data_ptr(), positions.data_ptr(), _addr(n_new), float(rope_theta),
+                int(rot_dims), pages, k.data_ptr(), v.data_ptr())
+        if fp8:
+            rc = lib().mimo_attn_cache_append_paged_fp8(*head, scales[0].data_ptr(), scales[1].data_ptr(), st)
+        else:
+            rc = lib().mimo_attn_cache_append_paged(*head, st)
+    _check("mimo_attn_cache_append_paged_fp8" if fp8 else "mimo_attn_cache_append_paged", rc)
+
+
+def cache_append_paged(k_new, v_new, k_pages, v_pages, block_table, positions, *, n_new=None, rope_theta=1e4,
+                       rot_dims=64, stream=None):
+    """mimo_attn_cache_append_paged: writes the new tokens' rotated K [B,n,Hkv,192] and V [B,n,Hkv,128]
+    into the pages, in place, from position positions[b] on (n_new [B]: only so many of them)."""
+    _append_paged(k_new, v_new, k_pages, v_pages, None, block_table, positions, n_new, rope_theta, rot_dims, stream)
+    return k_pages, v_pages
+
+
+def cache_append_paged_fp8(k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table, positions, *, n_new=None,
+                           rope_theta=1e4, rot_dims=64, stream=None):
+    """mimo_attn_cache_append_paged_fp8: as cache_append_paged(), into E4M3 pages (uint8) and their
+    scales [N,page,Hkv] fp32."""
+    _append_paged(k_new, v_new, k_pages, v_pages, (k_scale, v_scale), block_table, positions, n_new, rope_theta,
+                  rot_dims, stream)
+    return k_pages, v_pages, k_scale, v_scale
+
+
+def verify_drafts(target_probs, draft_tokens, uniforms, draft_probs=None, *, n_valid=None, n_accepted=None,
+                  tokens=None, stream=None):
+    """mimo_attn_verify_drafts. target_probs [B,T+1,V] fp32 or bf16, draft_tokens [B,T] int32, uniforms
+    [B,T+1] fp32, draft_probs [B,T,V] (None: drafts by argmax), n_valid [B] int32 or None. Returns
+    (n_accepted [B], tokens [B,T+1]) int32: the accepted drafts, the next token, then -1."""
+    dev = _cuda_device(target_probs, "target_probs")
+    if target_probs.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"target_probs must be float32 or bfloat16, got {target_probs.dtype}")
+    _need_at(target_probs, "target_probs", target_probs.dtype, (None, None, None), dev)
+    B, T1, V = target_probs.shape
+    T = T1 - 1
+    if T < 0:
+        raise ValueError("target_probs must have T + 1 rows per sequence")
+    _need_at(draft_tokens, "draft_tokens", torch.int32, (B, T), dev)
+    _need_at(uniforms, "uniforms", torch.float32, (B, T1), dev)
+    if draft_probs is not None:
+        _need_at(draft_probs, "draft_probs", target_probs.dtype, (B, T, V), dev)
+    if n_valid is not None:
+        _need_at(n_valid, "n_valid", torch.int32, (B,), dev)
+    if n_accepted is not None:
+        _need_at(n_accepted, "n_accepted", torch.int32, (B,), dev)
+    if tokens is not None:
+        _need_at(tokens, "tokens", torch.int32, (B, T1), dev)
+    with _On(dev, stream) as st:
+        if n_accepted is None:
+            n_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        if tokens is None:
+            tokens = torch.empty(B, T1, dtype=torch.int32, device=dev)
+        rc = lib().mimo_attn_verify_drafts(B, T, V, 0 if target_probs.dtype == torch.float32 else 1,
+                                           target_probs.data_ptr(), _addr(draft_probs), draft_tokens.data_ptr(),
+                                           uniforms.data_ptr(), _addr(n_valid), n_accepted.data_ptr(),
+                                           tokens.data_ptr(), st)
+    _check("mimo_attn_verify_drafts", rc)
+    return n_accepted, tokens
 
 
 def check_indices(lengths, sel_idx, *, hq, recent=128, capacity, stream=None):

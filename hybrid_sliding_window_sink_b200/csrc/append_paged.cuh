@@ -1,0 +1,157 @@
+// append_paged.cuh - writes new tokens into a paged KV cache: K rotated at its position, V as
+// it is, as bf16 or as E4M3 bytes with one scale per (token, KV head) row.
+//
+// Rotation ("...MiMo-V2.6-Flash-MOPD混合SWA设计原理" §5): dims (d, d + rot/2), d < rot/2, turn by
+// the angle pos * theta^(-2d/rot), reduced modulo 2 pi in double precision. FP8 rows: scale =
+// amax / 448 (1 for a row of zeros), byte = e4m3(x / scale), K from its rotated fp32 values.
+//
+// The bytes bound it (640 read and 640, or 328, written per row). A CTA takes kApTokens tokens
+// of one sequence with all their heads: the (cos, sin) of a token is computed once for its heads
+// (the frequencies theta^(-2d/rot) come from the host), and a warp writes one row at a time:
+// lanes 0-23 the 16-byte units of K (a unit's partner comes from its lane by a shuffle), lanes
+// 24-31 two units of V each, so a row's amax is a warp reduction.
+#pragma once
+
+#include "ptx.cuh"
+#include "decode.cuh"
+
+namespace mimo {
+
+constexpr int kApThreads = 256;
+
+struct AppendPagedParams {
+  const __nv_bfloat16* k;     // [B, n, Hkv, 192] un-rotated
+  const __nv_bfloat16* v;     // [B, n, Hkv, 128]
+  void* kc;                   // pages, as PagedParams
+  void* vc;
+  float* ks;                  // FP8 scales
+  float* vs;
+  const int* table;           // [B, max_pages]
+  const int* pos;             // [B] position of the chunk's first token
+  const int* n_new;           // [B] tokens to write (null: n)
+  long long page_stride;
+  int B, n, Hkv, rot, page_size, max_pages, num_pages, tokens;   // tokens: per CTA
+  double invf[kDQK / 2];      // theta^(-2d/rot)
+};
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+__device__ __forceinline__ void unpack8(const uint4 x, float (&f)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(w[i]);
+    f[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+__device__ __forceinline__ float amax8(const float (&f)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+  // fmaxf drops a NaN: keep it, so that the row's scale shows it
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = f[i] != f[i] ? f[i] : m;
+  return m;
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kApThreads) append_paged_kernel(const __grid_constant__ AppendPagedParams p) {
+  extern __shared__ float2 s_cs[];            // [tokens][rot / 2] (cos, sin)
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tiles = (p.n - 1) / p.tokens + 1;
+  const int b = blockIdx.x / tiles, i0 = (blockIdx.x - b * tiles) * p.tokens;
+  const int half = p.rot >> 1, nun = p.rot >> 4;   // nun: 16-byte units per half
+  int count = p.n_new ? min(__ldg(p.n_new + b), p.n) : p.n;
+  count = min(count - i0, p.tokens);
+  if (count <= 0) return;
+  const long long pos0 = static_cast<long long>(__ldg(p.pos + b)) + i0;
+  const long long most = static_cast<long long>(p.max_pages) * p.page_size;
+  for (int x = tid; x < count * half; x += kApThreads) {
+    const int t = x / half, d = x - t * half;
+    const double ang = static_cast<double>(pos0 + t) * p.invf[d];
+    const double turns = rint(ang * 0.15915494309189535);
+    float sn, cs;
+    sincosf(static_cast<float>(fma(-turns, 6.283185307179586, ang)), &sn, &cs);
+    s_cs[x] = make_float2(cs, sn);
+  }
+  __syncthreads();
+  for (int r = warp; r < count * p.Hkv; r += kApThreads / 32) {
+    const int t = r / p.Hkv, g = r - t * p.Hkv;
+    const long long pos = pos0 + t;
+    if (pos < 0 || pos >= most) continue;     // outside the table: not written
+    const int pg = static_cast<int>(pos / p.page_size);
+    const int ent = __ldg(p.table + static_cast<long long>(b) * p.max_pages + pg);
+    if (static_cast<unsigned>(ent) >= static_cast<unsigned>(p.num_pages)) continue;
+    const long long dst = (ent * p.page_stride + (pos - static_cast<long long>(pg) * p.page_size)) * p.Hkv + g;
+    const long long src = (static_cast<long long>(b) * p.n + i0 + t) * p.Hkv + g;
+    const bool is_k = lane < 24;
+    uint4 x0, x1 = make_uint4(0u, 0u, 0u, 0u);
+    if (is_k) {
+      x0 = *reinterpret_cast<const uint4*>(p.k + src * kDQK + lane * 8);
+    } else {
+      const uint4* pv = reinterpret_cast<const uint4*>(p.v + src * kDV + (lane - 24) * 16);
+      x0 = pv[0];
+      x1 = pv[1];
+    }
+    // the partner unit of the rotation, lane + nun or lane - nun
+    const int peer = lane < nun ? lane + nun : (lane < 2 * nun ? lane - nun : lane);
+    uint4 y;
+    y.x = __shfl_sync(0xffffffffu, x0.x, peer);
+    y.y = __shfl_sync(0xffffffffu, x0.y, peer);
+    y.z = __shfl_sync(0xffffffffu, x0.z, peer);
+    y.w = __shfl_sync(0xffffffffu, x0.w, peer);
+    float f[8], h[8];
+    unpack8(x0, f);
+    const bool turned = is_k && lane < 2 * nun;
+    if (turned) {
+      unpack8(y, h);
+      const float2* cs = s_cs + t * half + (lane < nun ? lane : lane - nun) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 w = cs[i];
+        f[i] = lane < nun ? f[i] * w.x - h[i] * w.y : f[i] * w.x + h[i] * w.y;
+      }
+    }
+    if constexpr (FP8) {
+      unpack8(x1, h);                         // V: second unit
+      // |x| orders as its bits, a NaN above all
+      const uint32_t bf = __float_as_uint(amax8(f)) & 0x7fffffffu, bh = __float_as_uint(amax8(h)) & 0x7fffffffu;
+      const float ak = __uint_as_float(__reduce_max_sync(0xffffffffu, is_k ? bf : 0u));
+      const float av = __uint_as_float(__reduce_max_sync(0xffffffffu, is_k ? 0u : max(bf, bh)));
+      float sk = ak / 448.f, sv = av / 448.f;
+      sk = sk == 0.f ? 1.f : sk;
+      sv = sv == 0.f ? 1.f : sv;
+      const float sc = is_k ? sk : sv;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[i] = f[i] / sc;
+        h[i] = h[i] / sc;
+      }
+      const uint2 lo = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+      if (is_k) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kc) + dst * kDQK + lane * 8) = lo;
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.vc) + dst * kDV + (lane - 24) * 16) =
+            make_uint4(lo.x, lo.y, e4m3x4(h[0], h[1], h[2], h[3]), e4m3x4(h[4], h[5], h[6], h[7]));
+      }
+      if (lane == 0) p.ks[dst] = sk;
+      if (lane == 24) p.vs[dst] = sv;
+    } else {
+      if (is_k) {
+        if (turned)
+          x0 = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.kc) + dst * kDQK + lane * 8) = x0;
+      } else {
+        uint4* pv = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.vc) + dst * kDV + (lane - 24) * 16);
+        pv[0] = x0;
+        pv[1] = x1;
+      }
+    }
+  }
+}
+
+}  // namespace mimo

@@ -22,6 +22,9 @@
 #include "prefill.cuh"
 #include "prefill_swa.cuh"
 #include "prefill_ga.cuh"
+#include "decode_paged.cuh"
+#include "append_paged.cuh"
+#include "verify.cuh"
 
 namespace mimo {
 
@@ -678,6 +681,197 @@ mimo_status launch_decode_mq_g(const mimo::DecodeMqParams& prm, cudaStream_t st)
   return launch_decode_mq_ring<G, 4>(prm, st);
 }
 
+// ---------------------------------------------------------------- paged KV cache
+mimo_status check_pages(const mimo_pages* pg) {
+  if (!pg) return MIMO_ERR_NULL;
+  if (pg->max_pages < 1 || pg->num_pages < 1 || pg->page_size < 1 || pg->page_stride_tokens < pg->page_size)
+    return MIMO_ERR_SHAPE;
+  if (static_cast<long long>(pg->max_pages) * pg->page_size > 0x7fffffffLL) return MIMO_ERR_UNSUPPORTED;
+  return MIMO_OK;
+}
+
+// CTAs of the paged decode (two per SM, resident at once) and its workspace: headers of the
+// units that a run boundary cuts, then two slots of G rows per CTA.
+struct PagedPlan {
+  int nctas;
+  bool split;               // a unit can be longer than one tile
+  size_t off_ml, off_o, bytes;
+};
+
+PagedPlan plan_paged(const mimo_shape* s, const mimo_pages* pg, int window, int n_first, bool fp8, int sms) {
+  PagedPlan pl{};
+  const long long G = s->n_q_heads / s->n_kv_heads;
+  const long long U = static_cast<long long>(s->batch) * s->n_kv_heads;
+  const int tile = fp8 ? mimo::PagedCfg<true>::KT : mimo::PagedCfg<false>::KT;
+  long long keys = static_cast<long long>(pg->max_pages) * pg->page_size;
+  if (window > 0) keys = std::min(keys, static_cast<long long>(window) + n_first);
+  pl.split = keys > tile;
+  const long long tiles = (keys + tile - 1) / tile;
+  pl.nctas = static_cast<int>(std::min<long long>(2LL * sms, U > 2LL * sms ? U : U * tiles));
+  if (!pl.split) return pl;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = 2 * static_cast<size_t>(pl.nctas) * G;
+  pl.off_ml = up(static_cast<size_t>(std::min<long long>(U, pl.nctas)) * sizeof(int4));
+  pl.off_o = pl.off_ml + up(rows * 2 * sizeof(float));
+  pl.bytes = pl.off_o + rows * mimo::kDV * sizeof(float);
+  return pl;
+}
+
+template <int G, bool FP8>
+mimo_status launch_paged(const mimo::PagedParams& prm, bool split, cudaStream_t st) {
+  auto kern = mimo::decode_paged_kernel<G, FP8>;
+  constexpr int smem = mimo::PagedCfg<FP8>::SMEM;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return MIMO_ERR_CUDA;
+  }
+  if (launch_pdl(kern, dim3(prm.nctas), mimo::kPgThreads, smem, st, prm, false) != cudaSuccess) return MIMO_ERR_CUDA;
+  const long long units = static_cast<long long>(prm.B) * prm.Hkv;
+  if (split && launch_pdl(mimo::decode_paged_combine_kernel,
+                          dim3(static_cast<unsigned>(std::min<long long>(units, prm.nctas)), G), 128, 0, st, prm) != cudaSuccess)
+    return MIMO_ERR_CUDA;
+  return MIMO_OK;
+}
+
+template <bool FP8>
+mimo_status run_paged(const mimo_shape* s, const void* q, const void* k, const void* v, const float* ks,
+                      const float* vs, const mimo_pages* pg, const int* lengths, int window, int n_first,
+                      const float* sink, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  mimo_status e = check_heads(s);
+  if (e != MIMO_OK) return e;
+  if (!q || !k || !v || !lengths || !out || !pg || !pg->block_table || (FP8 && (!ks || !vs))) return MIMO_ERR_NULL;
+  e = check_pages(pg);
+  if (e != MIMO_OK) return e;
+  if (n_first < 0) return MIMO_ERR_SHAPE;
+  if (static_cast<long long>(s->batch) * s->n_kv_heads > 0x7fffffffLL) return MIMO_ERR_UNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lengths, 4) ||
+      !aligned(pg->block_table, 4) || (sink && !aligned(sink, 4)) || (lse && !aligned(lse, 4)) ||
+      (FP8 && (!aligned(ks, 4) || !aligned(vs, 4))))
+    return MIMO_ERR_ALIGN;
+  const int dev = current_device();
+  if (dev < 0) return MIMO_ERR_CUDA;
+  const PagedPlan pl = plan_paged(s, pg, window, n_first, FP8, sm_count_for(dev));
+  if (pl.bytes > 0 && (!ws || ws_bytes < pl.bytes)) return MIMO_ERR_WORKSPACE;
+  if (ws && !aligned(ws, 16)) return MIMO_ERR_ALIGN;
+  mimo::PagedParams prm{};
+  prm.q = static_cast<const __nv_bfloat16*>(q);
+  prm.k = k;
+  prm.v = v;
+  prm.k_scale = ks;
+  prm.v_scale = vs;
+  prm.table = pg->block_table;
+  prm.lengths = lengths;
+  prm.sink = sink;
+  prm.out = static_cast<__nv_bfloat16*>(out);
+  prm.lse = lse;
+  if (pl.bytes > 0) {
+    prm.hdr = static_cast<int4*>(ws);
+    prm.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.off_ml);
+    prm.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.off_o);
+  }
+  prm.page_stride = pg->page_stride_tokens;
+  prm.B = s->batch;
+  prm.Hq = s->n_q_heads;
+  prm.Hkv = s->n_kv_heads;
+  prm.page_size = pg->page_size;
+  prm.max_pages = pg->max_pages;
+  prm.num_pages = pg->num_pages;
+  prm.window = window;
+  prm.n_first = n_first;
+  prm.nctas = pl.nctas;
+  // t / d = (t * m) >> (31 + l) for t < 2^31, with l = ceil(log2 d) and m = ceil(2^(31 + l) / d):
+  // m d exceeds 2^(31 + l) by less than d <= 2^l, so t's share of it stays below one step
+  int l = 0;
+  while ((1LL << l) < pg->page_size) ++l;
+  prm.div_shift = 31 + l;
+  prm.div_mul = static_cast<uint32_t>(((1ULL << (31 + l)) + pg->page_size - 1) / pg->page_size);
+  prm.scale_log2 = scale_log2_of(s);
+  prm.err = device_error_ptr(dev);
+  if (!prm.err) return MIMO_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (s->n_q_heads / s->n_kv_heads) {
+    case 1: return launch_paged<1, FP8>(prm, pl.split, st);
+    case 2: return launch_paged<2, FP8>(prm, pl.split, st);
+    case 4: return launch_paged<4, FP8>(prm, pl.split, st);
+    case 8: return launch_paged<8, FP8>(prm, pl.split, st);
+    default: return launch_paged<16, FP8>(prm, pl.split, st);
+  }
+}
+
+template <bool FP8>
+mimo_status run_append_paged(const mimo_shape* s, const void* k_new, const void* v_new, const int* positions,
+                             const int* n_new, float theta, int rot, const mimo_pages* pg, void* kc, void* vc,
+                             float* ks, float* vs, void* stream) {
+  mimo_status e = check_heads(s);
+  if (e != MIMO_OK) return e;
+  if (!k_new || !v_new || !positions || !kc || !vc || !pg || !pg->block_table || (FP8 && (!ks || !vs)))
+    return MIMO_ERR_NULL;
+  e = check_pages(pg);
+  if (e != MIMO_OK) return e;
+  if (s->seqlen < 1) return MIMO_ERR_SHAPE;
+  if (rot < 0 || rot > mimo::kDQK) return MIMO_ERR_SHAPE;
+  if (rot % 16) return MIMO_ERR_UNSUPPORTED;
+  if (rot > 0 && !(theta > 0.f && std::isfinite(theta))) return MIMO_ERR_SHAPE;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(kc, 16) || !aligned(vc, 16) || !aligned(positions, 4) ||
+      (n_new && !aligned(n_new, 4)) || !aligned(pg->block_table, 4) || (FP8 && (!aligned(ks, 4) || !aligned(vs, 4))))
+    return MIMO_ERR_ALIGN;
+  mimo::AppendPagedParams prm{};
+  // about 32 rows per CTA: four per warp
+  prm.tokens = std::max(1, std::min(std::min(s->seqlen, 32), 32 / s->n_kv_heads));
+  const long long blocks = static_cast<long long>(s->batch) * ((s->seqlen - 1) / prm.tokens + 1);
+  if (blocks > 0x7fffffffLL || static_cast<long long>(prm.tokens) * s->n_kv_heads > 0x7fffffffLL)
+    return MIMO_ERR_UNSUPPORTED;
+  if (current_device() < 0) return MIMO_ERR_CUDA;
+  prm.k = static_cast<const __nv_bfloat16*>(k_new);
+  prm.v = static_cast<const __nv_bfloat16*>(v_new);
+  prm.kc = kc;
+  prm.vc = vc;
+  prm.ks = ks;
+  prm.vs = vs;
+  prm.table = pg->block_table;
+  prm.pos = positions;
+  prm.n_new = n_new;
+  prm.page_stride = pg->page_stride_tokens;
+  prm.B = s->batch;
+  prm.n = s->seqlen;
+  prm.Hkv = s->n_kv_heads;
+  prm.rot = rot;
+  prm.page_size = pg->page_size;
+  prm.max_pages = pg->max_pages;
+  prm.num_pages = pg->num_pages;
+  for (int d = 0; d < rot / 2; ++d) prm.invf[d] = std::pow(static_cast<double>(theta), -2.0 * d / rot);
+  const size_t smem = static_cast<size_t>(prm.tokens) * (rot / 2) * sizeof(float2);   // <= 24 KB
+  mimo::append_paged_kernel<FP8><<<static_cast<unsigned>(blocks), mimo::kApThreads, smem, static_cast<cudaStream_t>(stream)>>>(prm);
+  return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- draft verification
+template <typename E>
+mimo_status launch_verify(mimo::VerifyParams prm, int B, cudaStream_t st) {
+  // a cluster of up to 8 CTAs shares a row; a short row takes fewer, so that a warp's piece
+  // keeps at least 64 tokens
+  int c = 1;
+  while (c < mimo::kVfMaxCluster && static_cast<long long>(c) * mimo::kVfWarps * 128 <= prm.V) c *= 2;
+  const int pieces = c * mimo::kVfWarps;
+  prm.piece = static_cast<int>(((static_cast<long long>(prm.V) + pieces - 1) / pieces + 31) / 32 * 32);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(c), static_cast<unsigned>(B));
+  cfg.blockDim = dim3(mimo::kVfThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, mimo::verify_kernel<E>, static_cast<const mimo::VerifyParams>(prm)) != cudaSuccess) {
+    cudaGetLastError();
+    return MIMO_ERR_CUDA;
+  }
+  return MIMO_OK;
+}
+
 }  // namespace
 
 // ============================================================== C ABI
@@ -978,6 +1172,73 @@ mimo_status mimo_attn_decode_mq(const mimo_shape* s, const void* q, const void* 
     case 8: return launch_decode_mq_g<8>(prm, st);
     default: return launch_decode_mq_g<16>(prm, st);
   }
+}
+
+size_t mimo_attn_decode_paged_workspace_size(const mimo_shape* s, const mimo_pages* pages, int window, int n_first) {
+  if (check_heads(s) != MIMO_OK || check_pages(pages) != MIMO_OK || n_first < 0) return 0;
+  if (static_cast<long long>(s->batch) * s->n_kv_heads > 0x7fffffffLL) return 0;
+  const int sms = sm_count_for(current_device());   // one size serves the bf16 and the FP8 call
+  return std::max(plan_paged(s, pages, window, n_first, false, sms).bytes,
+                  plan_paged(s, pages, window, n_first, true, sms).bytes);
+}
+
+mimo_status mimo_attn_decode_paged(const mimo_shape* s, const void* q, const void* k_pages, const void* v_pages,
+                                   const mimo_pages* pages, const int* lengths, int window, int n_first,
+                                   const float* sink, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  return run_paged<false>(s, q, k_pages, v_pages, nullptr, nullptr, pages, lengths, window, n_first, sink, out, lse,
+                          workspace, workspace_bytes, stream);
+}
+
+mimo_status mimo_attn_decode_paged_fp8(const mimo_shape* s, const void* q, const void* k_pages, const void* v_pages,
+                                       const float* k_scale, const float* v_scale, const mimo_pages* pages,
+                                       const int* lengths, int window, int n_first, const float* sink, void* out,
+                                       float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_paged<true>(s, q, k_pages, v_pages, k_scale, v_scale, pages, lengths, window, n_first, sink, out, lse,
+                         workspace, workspace_bytes, stream);
+}
+
+mimo_status mimo_attn_cache_append_paged(const mimo_shape* s, const void* k_new, const void* v_new,
+                                         const int* positions, const int* n_new, float rope_theta, int rot_dims,
+                                         const mimo_pages* pages, void* k_pages, void* v_pages, void* stream) {
+  return run_append_paged<false>(s, k_new, v_new, positions, n_new, rope_theta, rot_dims, pages, k_pages, v_pages,
+                                 nullptr, nullptr, stream);
+}
+
+mimo_status mimo_attn_cache_append_paged_fp8(const mimo_shape* s, const void* k_new, const void* v_new,
+                                             const int* positions, const int* n_new, float rope_theta, int rot_dims,
+                                             const mimo_pages* pages, void* k_pages, void* v_pages, float* k_scale,
+                                             float* v_scale, void* stream) {
+  return run_append_paged<true>(s, k_new, v_new, positions, n_new, rope_theta, rot_dims, pages, k_pages, v_pages,
+                                k_scale, v_scale, stream);
+}
+
+mimo_status mimo_attn_verify_drafts(int batch, int n_drafts, int vocab, int probs_type, const void* target_probs,
+                                    const void* draft_probs, const int* draft_tokens, const float* uniforms,
+                                    const int* n_valid, int* n_accepted, int* tokens, void* stream) {
+  if (!target_probs || !uniforms || !n_accepted || !tokens || (n_drafts > 0 && !draft_tokens)) return MIMO_ERR_NULL;
+  if (batch < 1 || n_drafts < 0 || vocab < 1) return MIMO_ERR_SHAPE;
+  if (probs_type != MIMO_PROBS_F32 && probs_type != MIMO_PROBS_BF16) return MIMO_ERR_SHAPE;
+  if (batch > 65535 || n_drafts == 0x7fffffff) return MIMO_ERR_UNSUPPORTED;
+  const uintptr_t pa = probs_type == MIMO_PROBS_F32 ? 4 : 2;
+  if (!aligned(target_probs, pa) || (draft_probs && !aligned(draft_probs, pa)) ||
+      (draft_tokens && !aligned(draft_tokens, 4)) || !aligned(uniforms, 4) || (n_valid && !aligned(n_valid, 4)) ||
+      !aligned(n_accepted, 4) || !aligned(tokens, 4))
+    return MIMO_ERR_ALIGN;
+  if (current_device() < 0) return MIMO_ERR_CUDA;
+  mimo::VerifyParams prm{};
+  prm.p = target_probs;
+  prm.q = n_drafts > 0 ? draft_probs : nullptr;
+  prm.draft = draft_tokens;
+  prm.u = uniforms;
+  prm.n_valid = n_valid;
+  prm.accepted = n_accepted;
+  prm.tokens = tokens;
+  prm.T = n_drafts;
+  prm.V = vocab;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return probs_type == MIMO_PROBS_F32 ? launch_verify<float>(prm, batch, st)
+                                      : launch_verify<__nv_bfloat16>(prm, batch, st);
 }
 
 size_t mimo_attn_decode_mq_workspace_size(const mimo_shape* s, int cache_kind, int cache_capacity,

@@ -1,0 +1,230 @@
+// verify.cuh - acceptance of drafted tokens against the target's probabilities.
+//
+// Math (speculative sampling, the step after the MTP verification pass of
+// "mimo-mtp-swa-not-mla"). For a sequence with drafts x_0 .. x_{n-1}, target rows p_0 .. p_n,
+// draft rows q_0 .. q_{n-1} (one-hot at x_t when none are given: drafts by argmax) and uniform
+// numbers u in [0, 1):
+//   accepted a = the first t with not (u_t q_t(x_t) < p_t(x_t)), or n;
+//   w(v) = max(p_a(v) - q_a(v), 0) for a < n, p_n(v) for a = n;
+//   next token = the smallest v with w(0) + .. + w(v) > u_T * sum w.
+// u q and p - q of fp32 values are exact in double, and the sums are double: at V = 131072 an
+// fp32 running sum is off by about as much as one token weighs (1e-5).
+//
+// Work: one row of p and one of q per sequence, read once (the accepted rows are only probed at
+// x_t), so the bytes bound it; for few sequences the latency of the steps does. A cluster of C
+// CTAs shares a row: warp k of the cluster's C * 16 sums one contiguous piece, the sums meet in
+// distributed shared memory, and the CTA of the piece that the target falls into reads that
+// piece again (from L2) with all its threads to find the token.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "ptx.cuh"
+
+namespace mimo {
+
+constexpr int kVfThreads = 512;
+constexpr int kVfWarps = kVfThreads / 32;
+constexpr int kVfMaxCluster = 8;
+
+struct VerifyParams {
+  const void* p;              // [B, T + 1, V] fp32 or bf16
+  const void* q;              // [B, T, V] or null (one-hot drafts)
+  const int* draft;           // [B, T]
+  const float* u;             // [B, T + 1]
+  const int* n_valid;         // [B] drafts to look at, or null (T)
+  int* accepted;              // [B]
+  int* tokens;                // [B, T + 1]
+  int T, V;
+  int piece;                  // elements per warp of the cluster
+};
+
+__device__ __forceinline__ float vf_load(const float* x) { return __ldg(x); }
+__device__ __forceinline__ float vf_load(const __nv_bfloat16* x) {
+  return __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(x))) << 16);
+}
+// The weight p - q of one token: differences that are not positive, and values that are not
+// finite, weigh nothing.
+__device__ __forceinline__ double vf_weight(float p, float q) {
+  const double w = static_cast<double>(p) - static_cast<double>(q);
+  return w > 0.0 && w <= 1.7976931348623157e308 ? w : 0.0;
+}
+__device__ __forceinline__ double vf_warp_sum(double x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ double vf_warp_scan(double x) {   // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+template <typename E>
+__global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams prm) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ double s_sum[kVfWarps];          // this CTA's piece sums (read by the cluster)
+  __shared__ double s_scan[kVfWarps];
+  __shared__ int s_acc, s_found;
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int T = prm.T, V = prm.V;
+  const E* p0 = static_cast<const E*>(prm.p) + static_cast<long long>(b) * (T + 1) * V;
+  const E* q0 = static_cast<const E*>(prm.q) + (prm.q ? static_cast<long long>(b) * T * V : 0);
+  const float* u = prm.u + static_cast<long long>(b) * (T + 1);
+  const int* draft = prm.draft + static_cast<long long>(b) * T;
+
+  int n = prm.n_valid ? __ldg(prm.n_valid + b) : T;
+  n = n < 0 ? 0 : (n < T ? n : T);
+  if (warp == 0) {                            // the first rejected draft, 32 at a time
+    int a = n;
+    for (int t0 = 0; t0 < n; t0 += 32) {
+      const int t = t0 + lane;
+      bool no = false;
+      if (t < n) {
+        const int x = __ldg(draft + t);
+        double px = 0.0, qx = prm.q ? 0.0 : 1.0;
+        if (x >= 0 && x < V) {                // a token outside the vocabulary is rejected
+          px = static_cast<double>(vf_load(p0 + static_cast<long long>(t) * V + x));
+          if (prm.q) qx = static_cast<double>(vf_load(q0 + static_cast<long long>(t) * V + x));
+        }
+        no = !(static_cast<double>(__ldg(u + t)) * qx < px);
+      }
+      const unsigned any = __ballot_sync(0xffffffffu, no);
+      if (any) {
+        a = t0 + __ffs(any) - 1;
+        break;
+      }
+    }
+    if (lane == 0) s_acc = a;
+  }
+  __syncthreads();
+  const int a = s_acc;
+  const E* p = p0 + static_cast<long long>(a) * V;
+  bool minus = a < n;                         // subtract the draft's row
+  const E* q = prm.q ? q0 + static_cast<long long>(a < T ? a : 0) * V : nullptr;
+  const int hot = minus && !prm.q ? __ldg(draft + a) : -1;
+  auto weight = [&](int v) -> double {
+    const float pv = vf_load(p + v);
+    float qv = 0.f;
+    if (minus) qv = q ? vf_load(q + v) : (v == hot ? 1.f : 0.f);
+    return vf_weight(pv, qv);
+  };
+
+  const int pieces = C * kVfWarps, mine = rank * kVfWarps + warp;
+  for (;;) {
+    const long long v0 = static_cast<long long>(mine) * prm.piece;
+    const long long v1 = min(v0 + prm.piece, static_cast<long long>(V));
+    double sum = 0.0;
+#pragma unroll 8
+    for (long long v = v0 + lane; v < v1; v += 32) sum += weight(static_cast<int>(v));
+    sum = vf_warp_sum(sum);
+    if (lane == 0) s_sum[warp] = sum;
+    cluster.sync();
+    // every warp finds the piece: lanes scan the sums, 32 at a time
+    double total = 0.0;
+    for (int i0 = 0; i0 < pieces; i0 += 32) {
+      const int i = i0 + lane;
+      double x = 0.0;
+      if (i < pieces) x = *cluster.map_shared_rank(&s_sum[i % kVfWarps], i / kVfWarps);
+      total += vf_warp_sum(x);
+    }
+    if (!(total > 0.0)) {
+      // nothing is left of p - q (p <= q everywhere): sample p itself; p without mass: no token
+      if (!minus) {
+        if (rank == 0 && tid == 0) {
+          prm.accepted[b] = a;
+          prm.tokens[static_cast<long long>(b) * (T + 1) + a] = -1;
+        }
+        break;
+      }
+      minus = false;
+      cluster.sync();                         // the sums are read before they are written again
+      continue;
+    }
+    const double target = static_cast<double>(__ldg(u + T)) * total;
+    double before = 0.0, run = 0.0;
+    int found = -1, last = -1;
+    double last_before = 0.0;
+    for (int i0 = 0; i0 < pieces && found < 0; i0 += 32) {
+      const int i = i0 + lane;
+      double x = 0.0;
+      if (i < pieces) x = *cluster.map_shared_rank(&s_sum[i % kVfWarps], i / kVfWarps);
+      const double incl = vf_warp_scan(x);
+      const unsigned hit = __ballot_sync(0xffffffffu, x > 0.0 && run + incl > target);
+      const unsigned some = __ballot_sync(0xffffffffu, x > 0.0);
+      const double excl = run + (incl - x);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        found = i0 + l;
+        before = __shfl_sync(0xffffffffu, excl, l);
+      } else if (some) {
+        const int l = 31 - __clz(some);
+        last = i0 + l;
+        last_before = __shfl_sync(0xffffffffu, excl, l);
+      }
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (found < 0) {                          // u = 1, or the sum's last rounding: the last piece with mass
+      found = last;
+      before = last_before;
+    }
+    if (found / kVfWarps == rank) {
+      // this CTA holds the piece: each thread takes a contiguous share of it
+      const long long w0 = static_cast<long long>(found) * prm.piece;
+      const int len = static_cast<int>(min(static_cast<long long>(prm.piece), V - w0));
+      const int share = (len + kVfThreads - 1) / kVfThreads;
+      const int e0 = min(tid * share, len), e1 = min(e0 + share, len);
+      double own = 0.0;
+      int top = -1;                           // last token of the share with mass
+      for (int e = e0; e < e1; ++e) {
+        const double w = weight(static_cast<int>(w0) + e);
+        own += w;
+        if (w > 0.0) top = e;
+      }
+      const double incl = vf_warp_scan(own);
+      if (lane == 31) s_scan[warp] = incl;
+      if (tid == 0) s_found = 0x7fffffff;
+      __syncthreads();
+      double at = before;
+      for (int w = 0; w < warp; ++w) at += s_scan[w];
+      at += incl - own;
+      int hit = 0x7fffffff;
+      for (int e = e0; e < e1; ++e) {
+        const double w = weight(static_cast<int>(w0) + e);
+        at += w;
+        if (w > 0.0 && at > target) {
+          hit = e;
+          break;
+        }
+      }
+      if (hit != 0x7fffffff) atomicMin(&s_found, hit);
+      __syncthreads();
+      const bool none = s_found == 0x7fffffff;
+      __syncthreads();
+      if (none) {                             // the last rounding again: the piece's last token with mass
+        if (tid == 0) s_found = -1;
+        __syncthreads();
+        if (top >= 0) atomicMax(&s_found, top);
+        __syncthreads();
+      }
+      if (tid == 0) {
+        prm.accepted[b] = a;
+        prm.tokens[static_cast<long long>(b) * (T + 1) + a] = static_cast<int>(w0) + s_found;
+      }
+    }
+    break;
+  }
+  if (rank == 0) {                            // the accepted drafts, and -1 behind the new token
+    for (int t = tid; t <= T; t += kVfThreads)
+      if (t != a) prm.tokens[static_cast<long long>(b) * (T + 1) + t] = t < a ? __ldg(draft + t) : -1;
+  }
+  cluster.sync();                             // no CTA leaves while its sums may be read
+}
+
+}  // namespace mimo

@@ -303,6 +303,120 @@ mimo_status mimo_attn_select_tokens(const mimo_shape* shape, const void* q, cons
                                     void* workspace, size_t workspace_bytes, void* stream);
 size_t mimo_attn_select_workspace_size(const mimo_shape* shape, int cache_capacity);
 
+/*
+ * A paged KV cache: a pool of num_pages pages of page_size tokens, and per sequence the list of
+ * its pages. Token t of sequence b is row block_table[b][t / page_size], t % page_size.
+ *
+ *  block_table        [B, max_pages] int32 device. Sequences may share pages. An entry outside
+ *                     [0, num_pages) (-1, say) names no page: its tokens are no keys of the decode
+ *                     and are not written by the append
+ *  max_pages          entries per sequence; max_pages * page_size < 2^31
+ *  num_pages          pages in the pool
+ *  page_size          tokens per page, any size >= 1
+ *  page_stride_tokens distance between pages in tokens (>= page_size), the same for K, V and scales
+ */
+typedef struct mimo_pages {
+  const int* block_table;
+  int max_pages;
+  int num_pages;
+  int page_size;
+  long long page_stride_tokens;
+} mimo_pages;
+
+/*
+ * One-token decode over a paged KV cache, optionally bounded by a sliding window with the first
+ * tokens kept visible. With L = lengths[b] (the query sits at position L - 1) the keys are
+ *   [0, min(n_first, lo)) and [lo, L), lo = max(0, L - window); window <= 0: all of [0, L).
+ * Pages between the two ranges are never read, so their entries may have been given up (-1).
+ *
+ *  q        [B, Hq, 192] bf16 device, already rotated at position L - 1
+ *  k_pages  [num_pages, page_stride_tokens, Hkv, 192] bf16 device, rotated K
+ *  v_pages  [num_pages, page_stride_tokens, Hkv, 128] bf16 device
+ *  lengths  [B] int32 device (clamped to [0, max_pages * page_size]); an empty key set gives
+ *           o = 0 and lse = sink (-inf without a sink)
+ *  n_first  first tokens that stay visible behind the window, >= 0
+ *  sink     [Hq] fp32 or NULL; out [B, Hq, 128] bf16 (written); lse [B, Hq] fp32 or NULL
+ *  workspace  at least mimo_attn_decode_paged_workspace_size(...) bytes (may be NULL when that is
+ *           0); calls that can overlap (two streams, two graphs replayed at once) need one each
+ *
+ * The work is cut into equal runs over all sequences, whatever their lengths, and joined by a
+ * second launch; results do not depend on timing. P is carried with 16 significant bits.
+ * Errors as mimo_attn_decode; MIMO_ERR_SHAPE also for the page sizes, MIMO_ERR_UNSUPPORTED for
+ * max_pages * page_size >= 2^31.
+ *
+ * _fp8: E4M3 bytes with one fp32 scale per (token, KV head) row of each tensor, as in
+ * mimo_attn_decode_fp8: k_pages / v_pages uint8, k_scale / v_scale [num_pages,
+ * page_stride_tokens, Hkv] fp32.
+ */
+mimo_status mimo_attn_decode_paged(const mimo_shape* shape, const void* q, const void* k_pages,
+                                   const void* v_pages, const mimo_pages* pages, const int* lengths,
+                                   int window, int n_first, const float* sink, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+mimo_status mimo_attn_decode_paged_fp8(const mimo_shape* shape, const void* q, const void* k_pages,
+                                       const void* v_pages, const float* k_scale, const float* v_scale,
+                                       const mimo_pages* pages, const int* lengths, int window,
+                                       int n_first, const float* sink, void* out, float* lse,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace the two paged decodes need for these sizes on the current device (0
+ * when none is needed or the arguments are invalid); pages->block_table is not looked at. */
+size_t mimo_attn_decode_paged_workspace_size(const mimo_shape* shape, const mimo_pages* pages, int window,
+                                             int n_first);
+
+/*
+ * Writes n = shape->seqlen new tokens of every sequence into a paged KV cache, as the paged
+ * decode reads it: token i of sequence b at position positions[b] + i, K rotated there (as
+ * mimo_attn_cache_append) and rounded to bf16, V copied. Everything else in the pool stays as it
+ * is.
+ *
+ *  k_new [B, n, Hkv, 192], v_new [B, n, Hkv, 128] bf16 device (un-rotated K)
+ *  positions [B] int32 device: position of a sequence's first new token
+ *  n_new     [B] int32 device: tokens to write, 0 .. n (a padded batch), or NULL: n each
+ *
+ * A token before position 0, behind the table, or on an entry that names no page is not written.
+ * Two tokens of one call must not share a row. _fp8: rows become E4M3 bytes and a scale amax / 448
+ * (1 for a row of zeros; a NaN in a row shows in its scale), K from its rotated fp32 values.
+ * Errors as mimo_attn_cache_append, and those of the page sizes above.
+ */
+mimo_status mimo_attn_cache_append_paged(const mimo_shape* shape, const void* k_new, const void* v_new,
+                                         const int* positions, const int* n_new, float rope_theta,
+                                         int rot_dims, const mimo_pages* pages, void* k_pages,
+                                         void* v_pages, void* stream);
+mimo_status mimo_attn_cache_append_paged_fp8(const mimo_shape* shape, const void* k_new, const void* v_new,
+                                             const int* positions, const int* n_new, float rope_theta,
+                                             int rot_dims, const mimo_pages* pages, void* k_pages,
+                                             void* v_pages, float* k_scale, float* v_scale, void* stream);
+
+enum { MIMO_PROBS_F32 = 0, MIMO_PROBS_BF16 = 1 };
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from given random numbers
+ * (speculative sampling; the step after the MTP verification pass of mimo_attn_decode_mq). Per
+ * sequence, with n = n_valid[b] drafts (all T = n_drafts when n_valid is NULL):
+ *   accepted a = the first t < n for which u[t] * q_t(x_t) < p_t(x_t) does not hold, or n;
+ *   w(v) = max(p_a(v) - q_a(v), 0) if a < n, p_n(v) if a = n;
+ *   next token = the smallest v with w(0) + .. + w(v) > u[T] * (sum of w).
+ * The rows need not sum to 1. Negative and non-finite weights count as 0. Where nothing is left
+ * of p_a - q_a, p_a itself is sampled; a target row without mass gives the token -1.
+ *
+ *  target_probs [B, T + 1, V] device; row t is the target's distribution of the token after t
+ *               accepted drafts. fp32 or bf16 (probs_type); sums are taken in double
+ *  draft_probs  [B, T, V] device, same type, or NULL: drafts chosen by argmax (q one-hot at x_t)
+ *  draft_tokens [B, T] int32 device (NULL allowed when T = 0); a token outside [0, V) is rejected
+ *  uniforms     [B, T + 1] fp32 device, in [0, 1); the last one draws the next token
+ *  n_valid      [B] int32 device (clamped to [0, T]) or NULL
+ *  n_accepted   [B] int32 device (written)
+ *  tokens       [B, T + 1] int32 device (written): the accepted drafts, the next token, then -1
+ *
+ * Errors: MIMO_ERR_NULL, MIMO_ERR_SHAPE (batch or vocab < 1, n_drafts < 0, an unknown type),
+ * MIMO_ERR_UNSUPPORTED (batch > 65535), MIMO_ERR_ALIGN (a pointer not aligned to its type; no
+ * 16-byte rule here), MIMO_ERR_CUDA. No workspace.
+ */
+mimo_status mimo_attn_verify_drafts(int batch, int n_drafts, int vocab, int probs_type,
+                                    const void* target_probs, const void* draft_probs,
+                                    const int* draft_tokens, const float* uniforms, const int* n_valid,
+                                    int* n_accepted, int* tokens, void* stream);
+
 /* Bytes of device workspace mimo_attn_decode / mimo_attn_sparse need for these sizes
  * on the current device (0 when none is needed). Returns 0 for invalid arguments. */
 size_t mimo_attn_workspace_size(const mimo_shape* shape, int op, int cache_kind,
