@@ -29,7 +29,7 @@ EXPORTS = ("mimo_attn_prefill", "mimo_attn_decode", "mimo_attn_sparse", "mimo_at
            "mimo_attn_decode_mq", "mimo_attn_decode_mq_workspace_size", "mimo_attn_workspace_size",
            "mimo_attn_decode_fp8", "mimo_attn_sparse_fp8", "mimo_attn_prefill_chunk",
            "mimo_attn_cache_append", "mimo_attn_select_tokens", "mimo_attn_select_workspace_size",
-           "mimo_attn_decode_paged", "mimo_attn_decode_paged_fp8", "mimo_attn_decode_paged_workspace_size",
+           "mimo_attn_prefill_first", "mimo_attn_decode_paged", "mimo_attn_decode_paged_fp8", "mimo_attn_decode_paged_workspace_size",
            "mimo_attn_cache_append_paged", "mimo_attn_cache_append_paged_fp8", "mimo_attn_verify_drafts",
            "mimo_attn_check_indices", "mimo_attn_last_device_error", "mimo_attn_device_status",
            "mimo_status_string", "mimo_attn_version")
@@ -89,6 +89,7 @@ def load(path):
     L.mimo_attn_select_workspace_size.restype = SZ
     L.mimo_attn_decode_fp8.argtypes = [SP, P, P, P, P, P, I, I, LL, P, P, P, P, P, SZ, P]
     L.mimo_attn_sparse_fp8.argtypes = [SP, P, P, P, P, P, I, LL, P, I, P, I, P, P, P, P, SZ, P]
+    L.mimo_attn_prefill_first.argtypes = [SP, P, P, P, I, I, P, I, I, F, I, P, P, P]
     PP = ctypes.POINTER(MimoPages)
     L.mimo_attn_decode_paged.argtypes = [SP, P, P, P, PP, P, I, I, P, P, P, P, SZ, P]
     L.mimo_attn_decode_paged_fp8.argtypes = [SP, P, P, P, P, P, PP, P, I, I, P, P, P, P, SZ, P]
@@ -475,6 +476,36 @@ def _cuda_device(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.device
+
+
+def prefill_first(q, k, v, sink=None, *, window, n_first, pos_offset=0, k_prefix_rotated=True, rope_theta=1e4,
+                  rot_dims=64, softmax_scale=0.0, out=None, lse=None, want_lse=True, stream=None):
+    """mimo_attn_prefill_first. q [B,n,Hq,192] at positions pos_offset on; k, v [B,pos_offset+n,Hkv,·]
+    (prefix K rotated when k_prefix_rotated). A query sees its last ``window`` tokens and the first
+    ``n_first``. Returns (out [B,n,Hq,128] bf16, lse [B,Hq,n] fp32 or None)."""
+    dev = _cuda_device(q, "q")
+    _need_at(q, "q", torch.bfloat16, (None, None, None, 192), dev)
+    B, n, hq = q.shape[:3]
+    _need_at(k, "k", torch.bfloat16, (B, pos_offset + n, None, 192), dev)
+    hkv = k.shape[2]
+    _need_at(v, "v", torch.bfloat16, (B, pos_offset + n, hkv, 128), dev)
+    if sink is not None:
+        _need_at(sink, "sink", torch.float32, (hq,), dev)
+    if out is not None:
+        _need_at(out, "out", torch.bfloat16, (B, n, hq, 128), dev)
+    if lse is not None:
+        _need_at(lse, "lse", torch.float32, (B, hq, n), dev)
+    shape = MimoShape(B, n, hq, hkv, 192, 128, float(softmax_scale))
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty(B, n, hq, 128, dtype=torch.bfloat16, device=dev)
+        if lse is None and want_lse:
+            lse = torch.empty(B, hq, n, dtype=torch.float32, device=dev)
+        rc = lib().mimo_attn_prefill_first(shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), int(pos_offset),
+                                           1 if k_prefix_rotated else 0, _addr(sink), int(window), int(n_first),
+                                           float(rope_theta), int(rot_dims), out.data_ptr(), _addr(lse), st)
+    _check("mimo_attn_prefill_first", rc)
+    return out, lse
 
 
 def _pages(k, v, table, scales=()):

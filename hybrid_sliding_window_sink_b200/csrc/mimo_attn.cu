@@ -195,7 +195,7 @@ bool make_tmap(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint6
 }
 
 // ---------------------------------------------------------------- prefill
-template <int G, int BN, int NKS>
+template <int G, int BN, int NKS, bool FIRST = false>
 mimo_status launch_prefill(const mimo_shape* s, const void* q, const void* k, const void* v,
                            PrefillParams prm, int sms, cudaStream_t st) {
   using C = mimo::PfCfg<G, BN, NKS>;
@@ -206,7 +206,7 @@ mimo_status launch_prefill(const mimo_shape* s, const void* q, const void* k, co
       !make_tmap(&tk, k, mimo::kDQK, s->n_kv_heads, nk, B, 1, BN) ||
       !make_tmap(&tv, v, mimo::kDV, s->n_kv_heads, nk, B, 1, BN))
     return MIMO_ERR_CUDA;
-  auto kern = mimo::prefill_kernel<G, BN, NKS>;
+  auto kern = mimo::prefill_kernel<G, BN, NKS, FIRST>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) {
     cudaGetLastError();
     return MIMO_ERR_CUDA;
@@ -303,6 +303,13 @@ mimo_status prefill_chunk_group(const mimo_shape* s, const void* q, const void* 
   }
   if (swa && P + prm.window - 1 <= 144) return launch_prefill<G, 144, 1>(s, q, k, v, prm, sms, st);
   return launch_prefill<G, 128, 2>(s, q, k, v, prm, sms, st);
+}
+
+// A window with the first n_first tokens kept visible.
+template <int G>
+mimo_status prefill_first_group(const mimo_shape* s, const void* q, const void* k, const void* v,
+                                const PrefillParams& prm, int sms, cudaStream_t st) {
+  return launch_prefill<G, 128, 2, true>(s, q, k, v, prm, sms, st);
 }
 
 // Launches a decode-side kernel, with programmatic stream serialization when `pdl` is set: its
@@ -681,6 +688,63 @@ mimo_status launch_decode_mq_g(const mimo::DecodeMqParams& prm, cudaStream_t st)
   return launch_decode_mq_ring<G, 4>(prm, st);
 }
 
+// Chunked prefill; n_first > 0: the first tokens stay visible behind the window.
+mimo_status run_prefill_chunk(const mimo_shape* s, const void* q, const void* k, const void* v, int pos_offset,
+                              int k_prefix_rotated, const float* sink, int window, int n_first, float rope_theta,
+                              int rot_dims, void* out, float* lse, void* stream) {
+  mimo_status e = check_heads(s);
+  if (e != MIMO_OK) return e;
+  if (!q || !k || !v || !out) return MIMO_ERR_NULL;
+  if (s->seqlen < 1 || pos_offset < 0) return MIMO_ERR_SHAPE;
+  if (static_cast<long long>(pos_offset) + s->seqlen > 0x7fffffffLL) return MIMO_ERR_UNSUPPORTED;
+  if (rot_dims < 0 || rot_dims > mimo::kDQK) return MIMO_ERR_SHAPE;
+  if (rot_dims % 16) return MIMO_ERR_UNSUPPORTED;
+  if (rot_dims > 0 && !(rope_theta > 0.f && std::isfinite(rope_theta))) return MIMO_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+      (sink && !aligned(sink, 4)) || (lse && !aligned(lse, 4)))
+    return MIMO_ERR_ALIGN;
+  const int dev = current_device();
+  if (dev < 0) return MIMO_ERR_CUDA;
+  PrefillParams prm{};
+  prm.sink = sink;
+  prm.out = static_cast<__nv_bfloat16*>(out);
+  prm.lse = lse;
+  prm.B = s->batch;
+  prm.n = s->seqlen;
+  prm.Hq = s->n_q_heads;
+  prm.Hkv = s->n_kv_heads;
+  prm.window = window;
+  prm.rot_dims = rot_dims;
+  prm.rope_theta = static_cast<double>(rope_theta);
+  prm.scale_log2 = scale_log2_of(s);
+  prm.q_off = pos_offset;
+  prm.nk = pos_offset + s->seqlen;
+  prm.krot_from = k_prefix_rotated ? pos_offset : 0;
+  prm.n_first = n_first;
+  prm.err = device_error_ptr(dev);
+  if (!prm.err) return MIMO_ERR_CUDA;
+  const int sms = sm_count_for(dev);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int group = s->n_q_heads / s->n_kv_heads;
+  // without a window that ends inside the keys, the first tokens are visible anyway
+  if (n_first > 0 && window > 0 && window < prm.nk) {
+    switch (group) {
+      case 1: return prefill_first_group<1>(s, q, k, v, prm, sms, st);
+      case 2: return prefill_first_group<2>(s, q, k, v, prm, sms, st);
+      case 4: return prefill_first_group<4>(s, q, k, v, prm, sms, st);
+      case 8: return prefill_first_group<8>(s, q, k, v, prm, sms, st);
+      default: return prefill_first_group<16>(s, q, k, v, prm, sms, st);
+    }
+  }
+  switch (group) {
+    case 1: return prefill_chunk_group<1>(s, q, k, v, prm, sms, st);
+    case 2: return prefill_chunk_group<2>(s, q, k, v, prm, sms, st);
+    case 4: return prefill_chunk_group<4>(s, q, k, v, prm, sms, st);
+    case 8: return prefill_chunk_group<8>(s, q, k, v, prm, sms, st);
+    default: return prefill_chunk_group<16>(s, q, k, v, prm, sms, st);
+  }
+}
+
 // ---------------------------------------------------------------- paged KV cache
 mimo_status check_pages(const mimo_pages* pg) {
   if (!pg) return MIMO_ERR_NULL;
@@ -927,45 +991,17 @@ mimo_status mimo_attn_prefill_chunk(const mimo_shape* s, const void* q, const vo
                                     int pos_offset, int k_prefix_rotated, const float* sink,
                                     int window, float rope_theta, int rot_dims, void* out,
                                     float* lse, void* stream) {
-  mimo_status e = check_heads(s);
-  if (e != MIMO_OK) return e;
-  if (!q || !k || !v || !out) return MIMO_ERR_NULL;
-  if (s->seqlen < 1 || pos_offset < 0) return MIMO_ERR_SHAPE;
-  if (static_cast<long long>(pos_offset) + s->seqlen > 0x7fffffffLL) return MIMO_ERR_UNSUPPORTED;
-  if (rot_dims < 0 || rot_dims > mimo::kDQK) return MIMO_ERR_SHAPE;
-  if (rot_dims % 16) return MIMO_ERR_UNSUPPORTED;
-  if (rot_dims > 0 && !(rope_theta > 0.f && std::isfinite(rope_theta))) return MIMO_ERR_SHAPE;
-  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
-      (sink && !aligned(sink, 4)) || (lse && !aligned(lse, 4)))
-    return MIMO_ERR_ALIGN;
-  const int dev = current_device();
-  if (dev < 0) return MIMO_ERR_CUDA;
-  PrefillParams prm{};
-  prm.sink = sink;
-  prm.out = static_cast<__nv_bfloat16*>(out);
-  prm.lse = lse;
-  prm.B = s->batch;
-  prm.n = s->seqlen;
-  prm.Hq = s->n_q_heads;
-  prm.Hkv = s->n_kv_heads;
-  prm.window = window;
-  prm.rot_dims = rot_dims;
-  prm.rope_theta = static_cast<double>(rope_theta);
-  prm.scale_log2 = scale_log2_of(s);
-  prm.q_off = pos_offset;
-  prm.nk = pos_offset + s->seqlen;
-  prm.krot_from = k_prefix_rotated ? pos_offset : 0;
-  prm.err = device_error_ptr(dev);
-  if (!prm.err) return MIMO_ERR_CUDA;
-  const int sms = sm_count_for(dev);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  switch (s->n_q_heads / s->n_kv_heads) {
-    case 1: return prefill_chunk_group<1>(s, q, k, v, prm, sms, st);
-    case 2: return prefill_chunk_group<2>(s, q, k, v, prm, sms, st);
-    case 4: return prefill_chunk_group<4>(s, q, k, v, prm, sms, st);
-    case 8: return prefill_chunk_group<8>(s, q, k, v, prm, sms, st);
-    default: return prefill_chunk_group<16>(s, q, k, v, prm, sms, st);
-  }
+  return run_prefill_chunk(s, q, k, v, pos_offset, k_prefix_rotated, sink, window, 0, rope_theta, rot_dims, out, lse,
+                           stream);
+}
+
+mimo_status mimo_attn_prefill_first(const mimo_shape* s, const void* q, const void* k, const void* v,
+                                    int pos_offset, int k_prefix_rotated, const float* sink,
+                                    int window, int n_first, float rope_theta, int rot_dims, void* out,
+                                    float* lse, void* stream) {
+  if (n_first < 0) return MIMO_ERR_SHAPE;
+  return run_prefill_chunk(s, q, k, v, pos_offset, k_prefix_rotated, sink, window, n_first, rope_theta, rot_dims, out,
+                           lse, stream);
 }
 
 mimo_status mimo_attn_cache_append(const mimo_shape* s, const void* k_chunk, const void* v_chunk,

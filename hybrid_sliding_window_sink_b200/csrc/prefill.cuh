@@ -25,6 +25,10 @@
 //              reduction, fp32 sin/cos, rotated dims kept as f16), sink-seeded
 //              online softmax from TMEM S,
 //              P (bf16) to shared memory, O rescale in TMEM, epilogue O / l -> bf16.
+// FIRST: a window with the first n_first tokens kept visible. The tiles of a row block are then
+// those of keys [0, min(n_first, lo)), if any, followed by those of [lo, p0+P-1]; keys below a
+// row's window are valid while they are below n_first, and a first tile ends at lo, so that no
+// key is met twice.
 // Every wait is bounded in time; on a timeout all roles leave their loops, the
 // producer and MMA thread wait (bounded) for their in-flight work, TMEM is freed
 // and the device error word is set.
@@ -50,6 +54,8 @@ struct PrefillParams {
   // cover positions 0 .. nk-1; key rows at positions < krot_from are stored rotated.
   // Whole-sequence prefill: q_off = 0, nk = n, krot_from = 0.
   int q_off, nk, krot_from;
+  // first tokens that stay visible behind a window (kernels instantiated with FIRST only)
+  int n_first;
   unsigned* err;
   unsigned long long* trace;   // debug timestamps (builds with -DMIMO_TRACE only), else null
 };
@@ -146,12 +152,13 @@ __device__ __forceinline__ void f16_row(uint32_t base, int chunk_bytes, int row,
   }
 }
 
-template <int G, int BN, int NKS>
+template <int G, int BN, int NKS, bool FIRST = false>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const PrefillParams p) {
   using C = PfCfg<G, BN, NKS>;
   static_assert(NKS == 1 || NKS == 2, "K stages");
+  static_assert(!FIRST || NKS == 2, "more than one tile per row block");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -210,11 +217,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       g = bg - b * p.Hkv;
     }
   };
+  int nft = 0;                                           // (FIRST) tiles of first tokens of the row block
   auto kv_range = [&](int qt, int& lo, int& ntiles) {
     const int p0 = p.q_off + qt * C::P;                  // absolute position of the block
     const int hi = min(p0 + C::P - 1, p.q_off + p.n - 1);
     lo = swa ? max(0, p0 - p.window + 1) : 0;
     ntiles = (hi - lo + BN) / BN;
+    if constexpr (FIRST) {
+      nft = (min(p.n_first, lo) + BN - 1) / BN;
+      ntiles += nft;
+    }
+  };
+  auto tile_key = [&](int j, int lo) -> int {            // first key of tile j
+    if constexpr (FIRST) return j < nft ? j * BN : lo + (j - nft) * BN;
+    return lo + j * BN;
   };
 
   if (warp == 0) {
@@ -236,12 +252,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const uint32_t sK = sK0 + ks * C::K_BYTES;
           mbar_arrive_expect_tx(bar(kBarKFull0 + ks), C::K_BYTES);
           for (int c = 0; c < 3; ++c)
-            tma_load_4d(sK + c * C::K_CHUNK, &tmK, bar(kBarKFull0 + ks), 64 * c, g, lo + j * BN, b);
+            tma_load_4d(sK + c * C::K_CHUNK, &tmK, bar(kBarKFull0 + ks), 64 * c, g, tile_key(j, lo), b);
           ++nk[ks];
           if (it >= 1 && !mbar_wait(bar(kBarVEmpty), (it - 1) & 1, s_abort, err)) { ok = false; break; }
           mbar_arrive_expect_tx(bar(kBarVFull), C::V_BYTES);
           for (int c = 0; c < 2; ++c)
-            tma_load_4d(sV + c * C::K_CHUNK, &tmV, bar(kBarVFull), 64 * c, g, lo + j * BN, b);
+            tma_load_4d(sV + c * C::K_CHUNK, &tmV, bar(kBarVFull), 64 * c, g, tile_key(j, lo), b);
           ++nv;
         }
         it_kv += T;
@@ -354,15 +370,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 
       const float sink2 = p.sink ? p.sink[h] * kLog2e : -INFINITY;
       float m = sink2, l = p.sink ? 1.f : 0.f;
-      if (!rope_k(it_kv, lo)) { ok = false; break; }
+      if (!rope_k(it_kv, tile_key(0, lo))) { ok = false; break; }
 
       for (int j = 0; j < T; ++j) {
         const int it = it_kv + j;
-        if (NKS >= 2 && j + 1 < T && !rope_k(it + 1, lo + (j + 1) * BN)) { ok = false; break; }
+        if (NKS >= 2 && j + 1 < T && !rope_k(it + 1, tile_key(j + 1, lo))) { ok = false; break; }
         if (!wait_all(bar(kBarSFull0 + (it & 1)), (it >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
         const uint32_t sc = trow + ((it & 1) ? C::S1_COL : 0);
-        const int kt0 = lo + j * BN;
+        const int kt0 = tile_key(j, lo);
+        const int khi = FIRST && j < nft ? lo - 1 : pos;   // last key this tile may contribute
+        auto key_ok = [&](int key) -> bool { return (key >= klo || (FIRST && key < p.n_first)) && key <= khi; };
 
         // pass 1: row max over the valid keys of this tile
         float mx = -INFINITY;
@@ -374,7 +392,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int key = kt0 + cb * 16 + e;
-            if (key >= klo && key <= pos) mx = fmaxf(mx, __uint_as_float(v[e]));
+            if (key_ok(key)) mx = fmaxf(mx, __uint_as_float(v[e]));
           }
         }
         const float mnew = fmaxf(m, mx * p.scale_log2);
@@ -397,7 +415,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int key = kt0 + cb * 16 + e;
-            const bool valid = key >= klo && key <= pos;
+            const bool valid = key_ok(key);
             pe[e] = valid ? ex2(__uint_as_float(v[e]) * p.scale_log2 - ref) : 0.f;
             sum += pe[e];
           }

@@ -304,6 +304,20 @@ mimo_status mimo_attn_select_tokens(const mimo_shape* shape, const void* q, cons
 size_t mimo_attn_select_workspace_size(const mimo_shape* shape, int cache_capacity);
 
 /*
+ * Prefill with a sliding window and pinned first tokens: as mimo_attn_prefill_chunk (whole
+ * sequences with pos_offset = 0), but the query at position i sees
+ *   J_i = [max(0, i - window + 1), i] and [0, n_first)
+ * (a token in both counts once). n_first >= 0, any size; n_first = 0, window <= 0 or window >=
+ * pos_offset + n is mimo_attn_prefill_chunk itself. Positions stay absolute: a first token keeps
+ * its own rotation. Errors as mimo_attn_prefill_chunk, MIMO_ERR_SHAPE also for n_first < 0.
+ * The decode of such a layer is mimo_attn_decode_paged with the same window and n_first.
+ */
+mimo_status mimo_attn_prefill_first(const mimo_shape* shape, const void* q, const void* k, const void* v,
+                                    int pos_offset, int k_prefix_rotated, const float* sink, int window,
+                                    int n_first, float rope_theta, int rot_dims, void* out, float* lse,
+                                    void* stream);
+
+/*
  * A paged KV cache: a pool of num_pages pages of page_size tokens, and per sequence the list of
  * its pages. Token t of sequence b is row block_table[b][t / page_size], t % page_size.
  *

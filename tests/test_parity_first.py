@@ -1,0 +1,151 @@
+"""Prefill with a sliding window and pinned first tokens against the float64 oracle.
+
+Bounds: the rotated dims of Q and K are carried in f16 (half a step 2^-11 each, on the products of
+64 dims), the weights in bf16 (2^-8), the output in bf16."""
+
+import numpy as np
+import pytest
+import torch
+
+from hybrid_sliding_window_sink_b200 import _lib, workloads as wl
+from oracle import serve
+from serve_util import BF16, F16, check, score_error
+
+SCALE = 192 ** -0.5
+
+
+def _inputs(B, n, off, hq, hkv, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    return {"q": (r(B, n, hq, 192) * scale).bfloat16(), "k": r(B, off + n, hkv, 192).bfloat16(),
+            "v": r(B, off + n, hkv, 128).bfloat16(), "sink": r(hq)}
+
+
+def _delta(inp, rot):
+    """Score error: that of the fp32 sums, and of rounding the rotated dims to f16, 2 * 2^-11 of the
+    magnitudes |q_r| |k_r| (Cauchy) of the rotated part."""
+    q, k = wl.to_f64(inp["q"]), wl.to_f64(inp["k"])
+    norm = lambda x: np.linalg.norm(x[..., :rot], axis=-1).max() if rot else 0.0  # noqa: E731
+    return score_error(q, k, SCALE) + 2.0 * F16 * SCALE * norm(q) * norm(k)
+
+
+def _check(inp, dev, window, first, off=0, rotated=False, theta=1e4, rot=64, sink=True, what=""):
+    d = {k: v.to(dev) for k, v in inp.items()}
+    out, lse = _lib.prefill_first(d["q"], d["k"], d["v"], d["sink"] if sink else None, window=window, n_first=first,
+                                  pos_offset=off, k_prefix_rotated=rotated, rope_theta=theta, rot_dims=rot)
+    torch.cuda.synchronize()
+    assert _lib.last_device_error() == 0
+    o, l, mass = serve.prefill_first(wl.to_f64(inp["q"]), wl.to_f64(inp["k"]), wl.to_f64(inp["v"]), off, rotated,
+                                     wl.to_f64(inp["sink"]) if sink else None, window, first, theta, rot)
+    check(out, lse, o, l, mass, BF16, _delta(inp, rot), what)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (16, 1), (16, 2), (4, 1), (4, 2), (2, 2)])
+@pytest.mark.parametrize("window,first", [(128, 4), (129, 16), (128, 17), (16, 1), (1, 3), (200, 64), (64, 150)])
+def test_heads_windows(cuda_device, hq, hkv, window, first):
+    _check(_inputs(1, 403, 0, hq, hkv, hq + window + first), cuda_device, window, first, what=f"{hq}/{hkv} {window} {first}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 127, 128, 129, 145, 300])
+def test_lengths(cuda_device, n):
+    _check(_inputs(2, n, 0, 16, 2, 50 + n), cuda_device, 128, 4, what=f"n={n}")
+    _check(_inputs(1, n, 0, 8, 1, 51 + n), cuda_device, 32, 20, sink=False, what=f"n={n}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("off,rotated", [(16, True), (160, False), (160, True), (333, True), (333, False), (2000, True)])
+@pytest.mark.parametrize("window,first", [(128, 4), (100, 16), (300, 5), (129, 140)])
+def test_chunks(cuda_device, off, rotated, window, first):
+    for hq, hkv in ((8, 1), (16, 1)):
+        _check(_inputs(1, 75, off, hq, hkv, off + window), cuda_device, window, first, off, rotated,
+               what=f"{hq}/{hkv} off {off} W {window} F {first}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rot,theta", [(0, 1e4), (16, 1e4), (64, 1e7), (128, 1e4), (192, 5e5)])
+def test_rotations(cuda_device, rot, theta):
+    for window, first in ((128, 4), (150, 40)):
+        _check(_inputs(1, 310, 0, 8, 1, rot), cuda_device, window, first, theta=theta, rot=rot, what=f"rot {rot}")
+
+
+@pytest.mark.gpu
+def test_many_blocks(cuda_device):
+    """Runs that cross sequences and heads, so that first tokens change hands inside a CTA."""
+    _check(_inputs(3, 700, 0, 16, 2, 60), cuda_device, 128, 4, what="3 x 700")
+    _check(_inputs(2, 520, 0, 32, 2, 61), cuda_device, 192, 130, what="2 x 520, G=16")
+
+
+@pytest.mark.gpu
+def test_peaked_and_dominant_sink(cuda_device):
+    inp = _inputs(1, 300, 0, 8, 1, 62, scale=8.0)
+    for window, first in ((128, 4), (160, 9)):
+        _check(inp, cuda_device, window, first, what="peaked")
+    inp["sink"] += 60
+    for window, first in ((128, 4), (160, 9)):
+        _check(inp, cuda_device, window, first, what="dominant sink")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,window,first", [(16, 2, 128, 4), (16, 1, 256, 32), (8, 2, 64, 64)])
+def test_long_sampled(cuda_device, hq, hkv, window, first):
+    """Every CTA holds several blocks; the oracle runs on the last 40 rows as a chunk."""
+    n = 9001
+    inp = _inputs(1, n, 0, hq, hkv, 63)
+    d = {k: v.to(cuda_device) for k, v in inp.items()}
+    out, lse = _lib.prefill_first(d["q"], d["k"], d["v"], d["sink"], window=window, n_first=first)
+    torch.cuda.synchronize()
+    assert _lib.last_device_error() == 0
+    for at in (0, 4321, n - 40):
+        end = at + 40
+        o, l, mass = serve.prefill_first(wl.to_f64(inp["q"][:, at:end]), wl.to_f64(inp["k"][:, :end]),
+                                         wl.to_f64(inp["v"][:, :end]), at, False, wl.to_f64(inp["sink"]), window, first,
+                                         1e4, 64)
+        check(out[:, at:end], lse[:, :, at:end], o, l, mass, BF16, _delta(inp, 64), f"rows {at}")
+
+
+@pytest.mark.gpu
+def test_chunks_are_the_whole(cuda_device):
+    """Chunk by chunk over raw keys gives the rows of one call (the same tiles up to their borders:
+    both within their bounds of the same numbers)."""
+    inp = {k: v.to(cuda_device) for k, v in _inputs(1, 512, 0, 8, 1, 64).items()}
+    want, _ = _lib.prefill_first(inp["q"], inp["k"], inp["v"], inp["sink"], window=128, n_first=4)
+    for lo, hi in ((0, 100), (100, 256), (256, 512)):
+        got, _ = _lib.prefill_first(inp["q"][:, lo:hi].contiguous(), inp["k"][:, :hi].contiguous(),
+                                    inp["v"][:, :hi].contiguous(), inp["sink"], window=128, n_first=4, pos_offset=lo,
+                                    k_prefix_rotated=False)
+        torch.cuda.synchronize()
+        tol = 4 * BF16 * want[:, lo:hi].float().abs() + 0.02
+        assert ((got.float() - want[:, lo:hi].float()).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+def test_without_first_tokens_is_the_chunk_call(cuda_device):
+    inp = {k: v.to(cuda_device) for k, v in _inputs(1, 300, 0, 8, 1, 65).items()}
+    for window, first in ((128, 0), (0, 9), (300, 9), (5000, 9)):
+        a = _lib.prefill_first(inp["q"], inp["k"], inp["v"], inp["sink"], window=window, n_first=first)
+        b = _lib.prefill_chunk(inp["q"], inp["k"], inp["v"], inp["sink"], pos_offset=0, window=window)
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.gpu
+def test_repeats_streams_graph(cuda_device):
+    inp = {k: v.to(cuda_device) for k, v in _inputs(1, 500, 0, 8, 1, 66).items()}
+    for window, first in ((128, 4), (200, 40)):
+        call = lambda **kw: _lib.prefill_first(inp["q"], inp["k"], inp["v"], inp["sink"], window=window,  # noqa: E731
+                                               n_first=first, **kw)
+        want = call()
+        side = torch.cuda.Stream(cuda_device)
+        side.wait_stream(torch.cuda.current_stream())
+        other = call(stream=side)
+        out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(out=out, lse=lse)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got in (other, (out, lse), call()):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

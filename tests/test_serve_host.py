@@ -177,3 +177,19 @@ def test_oracle_verify_by_hand():
     assert run(0, [0.99, 0.999]) == ([1], [[0, 2]])
     one = tuple(x.tolist() for x in serve.verify_drafts(p, None, np.array([[0]]), np.array([[0.6, 0.0]])))
     assert one == ([0], [[1, -1]])                        # argmax drafts: accepted with p(x), x leaves the rest
+
+
+def test_prefill_first_rejects(L):
+    def call(shape=None, q=GOOD, k=GOOD, v=GOOD, off=0, sink=None, window=128, first=4, theta=1e4, rot=64, out=GOOD,
+             lse=None):
+        return L.mimo_attn_prefill_first(_shape() if shape is None else shape, q, k, v, off, 0, sink, window, first,
+                                         theta, rot, out, lse, None)
+    for name in ("q", "k", "v", "out"):
+        assert call(**{name: None}) == 1, name
+        assert call(**{name: ODD}) == 4, name
+    assert call(sink=ODD) == 4 and call(lse=ODD) == 4
+    assert call(first=-1) == 2 and call(off=-1) == 2 and call(shape=_shape(seqlen=0)) == 2
+    assert call(off=2 ** 31 - 2) == 3 and call(shape=_shape(hq=3)) == 3 and call(rot=8) == 3
+    assert call(rot=-16) == 2 and call(rot=208) == 2 and call(theta=0.0) == 2
+    with pytest.raises(ValueError, match="CUDA"):
+        _lib.prefill_first(torch.zeros(1, 2, 8, 192).bfloat16(), None, None, window=1, n_first=1)
