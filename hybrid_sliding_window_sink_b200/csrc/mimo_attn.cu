@@ -221,9 +221,10 @@ mimo_status launch_prefill(const mimo_shape* s, const void* q, const void* k, co
 }
 
 // SWA layer with 8 query heads per KV head, W <= 129, rot_dims <= 64: the ring kernel.
+template <bool FIRST = false>
 mimo_status launch_prefill_swa(const mimo_shape* s, const void* q, const void* k, const void* v,
                                PrefillParams prm, int sms, cudaStream_t st) {
-  using L = mimo::SwaLayout;
+  using L = mimo::SwaLayout<FIRST>;
   CUtensorMap tq, tk, tv;
   const uint64_t n = static_cast<uint64_t>(s->seqlen), B = static_cast<uint64_t>(s->batch);
   const uint64_t nk = static_cast<uint64_t>(prm.nk);   // keys: n, or prefix + chunk
@@ -232,7 +233,7 @@ mimo_status launch_prefill_swa(const mimo_shape* s, const void* q, const void* k
       !make_tmap(&tk, k, mimo::kDQK, s->n_kv_heads, nk, B, 1, 16) ||
       !make_tmap(&tv, v, mimo::kDV, s->n_kv_heads, nk, B, 1, 16))
     return MIMO_ERR_CUDA;
-  if (cudaFuncSetAttribute(mimo::prefill_swa_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(mimo::prefill_swa_kernel<FIRST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            L::SMEM) != cudaSuccess) {
     cudaGetLastError();
     return MIMO_ERR_CUDA;
@@ -242,13 +243,13 @@ mimo_status launch_prefill_swa(const mimo_shape* s, const void* q, const void* k
   if (work > 0x7fffffffLL) return MIMO_ERR_UNSUPPORTED;
   prm.num_work = static_cast<int>(work);
   const int grid = prm.num_work < sms ? prm.num_work : sms;
-  mimo::prefill_swa_kernel<<<grid, mimo::kSwaThreads, L::SMEM, st>>>(tq, tk, tv, prm);
+  mimo::prefill_swa_kernel<FIRST><<<grid, mimo::kSwaThreads, L::SMEM, st>>>(tq, tk, tv, prm);
   return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
 }
 
 // Full causal prefix (GA layers) with 8 or 16 query heads per KV head, rot_dims <= 64:
 // two row blocks per work item share every K/V tile.
-template <int G>
+template <int G, bool WIN = false>
 mimo_status launch_prefill_ga(const mimo_shape* s, const void* q, const void* k, const void* v,
                               PrefillParams prm, int sms, cudaStream_t st) {
   using L = mimo::GaLayout<G>;
@@ -259,7 +260,7 @@ mimo_status launch_prefill_ga(const mimo_shape* s, const void* q, const void* k,
       !make_tmap(&tk, k, mimo::kDQK, s->n_kv_heads, nk, B, 1, mimo::kGaBN) ||
       !make_tmap(&tv, v, mimo::kDV, s->n_kv_heads, nk, B, 1, mimo::kGaBN))
     return MIMO_ERR_CUDA;
-  auto kern = mimo::prefill_ga_kernel<G>;
+  auto kern = mimo::prefill_ga_kernel<G, WIN>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess) {
     cudaGetLastError();
     return MIMO_ERR_CUDA;
@@ -305,10 +306,18 @@ mimo_status prefill_chunk_group(const mimo_shape* s, const void* q, const void* 
   return launch_prefill<G, 128, 2>(s, q, k, v, prm, sms, st);
 }
 
-// A window with the first n_first tokens kept visible.
+// A window with the first n_first tokens kept visible: the ring kernel where its window and
+// first tokens fit (its row blocks read each key once per run), the pair kernel for the other
+// windows of 8 and 16 heads per KV head, the generic kernel for the rest.
 template <int G>
 mimo_status prefill_first_group(const mimo_shape* s, const void* q, const void* k, const void* v,
                                 const PrefillParams& prm, int sms, cudaStream_t st) {
+  if (G == mimo::kSwaG && prm.window <= 129 && prm.n_first <= mimo::kSwaFirst && prm.rot_dims <= 64 &&
+      prm.q_off % mimo::kSwaP == 0)
+    return launch_prefill_swa<true>(s, q, k, v, prm, sms, st);
+  if constexpr (G == 8 || G == 16) {
+    if (prm.rot_dims <= 64) return launch_prefill_ga<G, true>(s, q, k, v, prm, sms, st);
+  }
   return launch_prefill<G, 128, 2, true>(s, q, k, v, prm, sms, st);
 }
 
@@ -721,6 +730,7 @@ mimo_status run_prefill_chunk(const mimo_shape* s, const void* q, const void* k,
   prm.nk = pos_offset + s->seqlen;
   prm.krot_from = k_prefix_rotated ? pos_offset : 0;
   prm.n_first = n_first;
+  prm.v = static_cast<const __nv_bfloat16*>(v);
   prm.err = device_error_ptr(dev);
   if (!prm.err) return MIMO_ERR_CUDA;
   const int sms = sm_count_for(dev);

@@ -54,8 +54,10 @@ struct PrefillParams {
   // cover positions 0 .. nk-1; key rows at positions < krot_from are stored rotated.
   // Whole-sequence prefill: q_off = 0, nk = n, krot_from = 0.
   int q_off, nk, krot_from;
-  // first tokens that stay visible behind a window (kernels instantiated with FIRST only)
+  // first tokens that stay visible behind a window (kernels instantiated with FIRST only), and
+  // the V rows as the caller gave them
   int n_first;
+  const __nv_bfloat16* v;  // [B, nk, Hkv, 128]
   unsigned* err;
   unsigned long long* trace;   // debug timestamps (builds with -DMIMO_TRACE only), else null
 };
@@ -151,6 +153,25 @@ __device__ __forceinline__ void f16_row(uint32_t base, int chunk_bytes, int row,
                  bf16x2_to_f16x2(x[3]));
   }
 }
+
+// Whether a V row [128] holds a NaN or an infinity. A weight of 0 does not hide such a value in
+// the PV product (0 * NaN), so a kernel that masks keys inside a tile replaces the row by zeros
+// and puts a NaN into the key's K row instead: the score is then NaN for every query row, masked
+// rows drop it, and the rows that do see the key become NaN.
+__device__ __forceinline__ bool v_row_not_finite(const __nv_bfloat16* row) {
+  const uint4* r = reinterpret_cast<const uint4*>(row);
+  const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+  __nv_bfloat162 acc = zero;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    const uint4 x = __ldg(r + u);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), zero, acc);
+  }
+  return !__hbeq2(acc, zero);
+}
+constexpr uint16_t kNan16 = 0x7fffu;      // a NaN in bf16 and in f16
 
 template <int G, int BN, int NKS, bool FIRST = false>
 __global__ void __launch_bounds__(kPfThreads, 1)
@@ -335,7 +356,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const bool w_ok = mbar_wait(b_, par, s_abort, err);
       return __all_sync(0xffffffffu, w_ok);
     };
-    auto rope_k = [&](int it, int key0) -> bool {
+    bool v_bad[2] = {false, false};                     // (FIRST) V row ctid of tile it & 1 is not finite
+    auto rope_k = [&](int it, int key0, int b, int g) -> bool {
       const int ks = it % NKS;
       if (!wait_all(bar(kBarKFull0 + ks), (it / NKS) & 1)) return false;
       if (p.rot_dims > 0) {
@@ -346,6 +368,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           else if (pos >= 0 && pos < p.krot_from) f16_row(sK, C::K_CHUNK, t, p.rot_dims);
         }
         fence_proxy_async_smem();
+      }
+      if constexpr (FIRST) {
+        static_assert(!FIRST || BN == 128, "one K row per thread");
+        const int pos = key0 + ctid;
+        const bool bad =
+            pos < p.nk && v_row_not_finite(p.v + ((static_cast<long long>(b) * p.nk + pos) * p.Hkv + g) * 128);
+        v_bad[it & 1] = bad;
+        if (bad) {
+          *reinterpret_cast<uint16_t*>(smem + C::OFF_K + ks * C::K_BYTES + ctid * 128 + ((ctid & 7) << 4)) = kNan16;
+          fence_proxy_async_smem();
+        }
       }
       mbar_arrive(bar(kBarKReady0 + ks));
       return true;
@@ -370,11 +403,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 
       const float sink2 = p.sink ? p.sink[h] * kLog2e : -INFINITY;
       float m = sink2, l = p.sink ? 1.f : 0.f;
-      if (!rope_k(it_kv, tile_key(0, lo))) { ok = false; break; }
+      if (!rope_k(it_kv, tile_key(0, lo), b, g)) { ok = false; break; }
 
       for (int j = 0; j < T; ++j) {
         const int it = it_kv + j;
-        if (NKS >= 2 && j + 1 < T && !rope_k(it + 1, tile_key(j + 1, lo))) { ok = false; break; }
+        if (NKS >= 2 && j + 1 < T && !rope_k(it + 1, tile_key(j + 1, lo), b, g)) { ok = false; break; }
         if (!wait_all(bar(kBarSFull0 + (it & 1)), (it >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
         const uint32_t sc = trow + ((it & 1) ? C::S1_COL : 0);
@@ -445,6 +478,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         l = l * alpha + sum;
         m = mnew;
+        if constexpr (FIRST) {
+          // zeros for the V rows that rope_k marked (PV starts only after this thread's arrival);
+          // the whole warp waits, as every wait here
+          if (__any_sync(0xffffffffu, v_bad[it & 1])) {
+            if (!wait_all(bar(kBarVFull), it & 1)) { ok = false; break; }
+            if (v_bad[it & 1])
+              for (int u = 0; u < 16; ++u)
+                *reinterpret_cast<uint4*>(smem + C::OFF_V + (u >> 3) * C::K_CHUNK + ctid * 128 + (u & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(bar(kBarPReady));

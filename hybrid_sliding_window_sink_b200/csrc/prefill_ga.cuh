@@ -19,6 +19,10 @@
 //                S in [0, 128) (P, bf16, overwrites it in [0, 64)) and O in [128, 256).
 // The MMA issues S_w of tile j+1 only after PV_w of tile j has completed (P aliases S),
 // so a softmax group always finds its O stable and never waits for PV inside a row block.
+// WIN: a window (any width) with the first n_first tokens kept visible. An item's tiles are then
+// the 128-key tiles of the first tokens that lie before its window, followed by those from the
+// one holding the lowest key of its window on; only tiles that some row masks in part pay for
+// masks, and for a look at their V rows (see v_row_not_finite).
 // Lazy rescaling: a row keeps its reference max until a tile raises it by more than 8 (log2
 // units); P = 2^(a - ref) then stays below 2^8, and O / l are rescaled only when the
 // reference moves.
@@ -99,10 +103,14 @@ enum : int {
   kGaPVDone = 15,  // [2]
   kGaBase = 17,    // [4] K-tile base table written (32 arrivals)
   kGaFinal = 21,
-  kGaNumBars = 22
+  // (WIN) V of a partly masked tile: landed, and its rows looked at (128 arrivals). Barriers of
+  // their own, so that the RoPE group, which passes over the other tiles' V, meets every phase
+  kGaVLook = 22,
+  kGaVReady = 23,
+  kGaNumBars = 24
 };
 
-template <int G>
+template <int G, bool WIN = false>
 __global__ void __launch_bounds__(kGaThreads, 1)
     prefill_ga_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const PrefillParams p) {
@@ -128,7 +136,7 @@ __global__ void __launch_bounds__(kGaThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kGaNumBars; ++i) {
       uint32_t cnt = 1;
-      if (i == kGaQReady || (i >= kGaKReady && i < kGaKReady + 2) || (i >= kGaPReady && i < kGaPReady + 2))
+      if (i == kGaQReady || i == kGaVReady || (i >= kGaKReady && i < kGaKReady + 2) || (i >= kGaPReady && i < kGaPReady + 2))
         cnt = 128;
       if (i >= kGaBase && i < kGaBase + 4) cnt = 32;
       mbar_init(bar(i), cnt);
@@ -165,6 +173,7 @@ __global__ void __launch_bounds__(kGaThreads, 1)
            ((r & 1) ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
   };
   // item w: longest first; (b, g) fastest so that concurrent CTAs share K/V tiles in L2
+  int nft = 0, t0 = 0;   // (WIN) tiles of first tokens of the last item asked for, and its window's first tile
   auto item_of = [&](int w, int& b, int& g, int& p0, int& ntiles) {
     const int bg = w % BG;
     const int pi = npairs - 1 - w / BG;
@@ -173,12 +182,26 @@ __global__ void __launch_bounds__(kGaThreads, 1)
     p0 = pi * 2 * P;                               // first query row of block A in the call
     const int hi = p.q_off + min(p0 + 2 * P - 1, p.n - 1);   // last position of the item
     ntiles = hi / kGaBN + 1;
+    if constexpr (WIN) {
+      t0 = max(0, p.q_off + p0 - p.window + 1) / kGaBN;
+      nft = min((p.n_first - 1) / kGaBN + 1, t0);
+      ntiles += nft - t0;
+    }
+  };
+  auto tile_of = [&](int j, int nf, int tw) -> int {   // 128-key tile j of an item
+    if constexpr (WIN) return j < nf ? j : tw + (j - nf);
+    return j;
+  };
+  // (WIN) whether some row of positions [plo, phi] masks a key of the tile at kt0
+  auto partly = [&](int kt0, int plo, int phi) -> bool {
+    return kt0 + kGaBN - 1 > plo || (kt0 < phi - p.window + 1 && kt0 + kGaBN > p.n_first);
   };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       int nq = 0, nk = 0, nv = 0;   // loads issued
+      int nlook = 0;                // (WIN) those of nv on kGaVLook
       bool ok = true;
       for (int rd = 0, w = work_of(0); w < p.num_work && ok; w = work_of(++rd)) {
         int b, g, p0, T;
@@ -200,14 +223,21 @@ __global__ void __launch_bounds__(kGaThreads, 1)
             mbar_arrive_expect_tx(bar(kGaKFull + ks), L::K_TILE);
             for (int c = 0; c < 3; ++c)
               tma_load_4d(sK + ks * L::K_TILE + c * L::K_CHUNK, &tmK, bar(kGaKFull + ks), 64 * c, g,
-                          j * kGaBN, b);
+                          tile_of(j, nft, t0) * kGaBN, b);
             ++nk;
           }
           if (j >= 1) {
             if (nv >= 1 && !mbar_wait(bar(kGaVEmpty), (nv - 1) & 1, s_abort, err)) { ok = false; break; }
-            mbar_arrive_expect_tx(bar(kGaVFull), L::V_TILE);
+            int vbar = kGaVFull;
+            if constexpr (WIN) {
+              if (partly(tile_of(j - 1, nft, t0) * kGaBN, p.q_off + p0, p.q_off + p0 + 2 * P - 1)) {
+                vbar = kGaVLook;
+                ++nlook;
+              }
+            }
+            mbar_arrive_expect_tx(bar(vbar), L::V_TILE);
             for (int c = 0; c < 2; ++c)
-              tma_load_4d(sV + c * L::K_CHUNK, &tmV, bar(kGaVFull), 64 * c, g, (j - 1) * kGaBN, b);
+              tma_load_4d(sV + c * L::K_CHUNK, &tmV, bar(vbar), 64 * c, g, tile_of(j - 1, nft, t0) * kGaBN, b);
             ++nv;
           }
         }
@@ -216,7 +246,8 @@ __global__ void __launch_bounds__(kGaThreads, 1)
         if (nq > 0) mbar_wait_drain(bar(kGaQFull), (nq - 1) & 1, err);
         for (int t = nk - 2 < 0 ? 0 : nk - 2; t < nk; ++t)
           mbar_wait_drain(bar(kGaKFull + (t & 1)), (t >> 1) & 1, err);
-        if (nv > 0) mbar_wait_drain(bar(kGaVFull), (nv - 1) & 1, err);
+        if (nv - nlook > 0) mbar_wait_drain(bar(kGaVFull), (nv - nlook - 1) & 1, err);
+        if (nlook > 0) mbar_wait_drain(bar(kGaVLook), (nlook - 1) & 1, err);
       }
     }
   } else if (warp == 1) {
@@ -229,6 +260,10 @@ __global__ void __launch_bounds__(kGaThreads, 1)
       bool s_done = s_w >= p.num_work, v_done = v_w >= p.num_work;
       if (!s_done) item_of(s_w, b_, g_, p0_, s_T);
       if (!v_done) item_of(v_w, b_, g_, p0_, v_T);
+      int v_p0 = v_done ? 0 : p0_, v_nft = nft, v_t0 = t0, v_cleaned = 0;   // (WIN)
+      auto v_partly = [&]() -> bool {
+        return partly(tile_of(v_j, v_nft, v_t0) * kGaBN, p.q_off + v_p0, p.q_off + v_p0 + 2 * P - 1);
+      };
       bool ok = true;
       uint32_t idle = 0;
       unsigned long long t_prog = globaltimer_ns();
@@ -272,7 +307,15 @@ __global__ void __launch_bounds__(kGaThreads, 1)
         }
         if (v_gt < s_gt || (v_gt == s_gt && v_grp < s_grp)) {   // PV only after its S
           bool ready = mbar_test(bar(kGaPReady + v_grp), v_gt & 1);
-          if (ready && v_grp == 0) ready = mbar_test(bar(kGaVFull), v_gt & 1);
+          if constexpr (WIN) {
+            if (ready && v_grp == 0) {
+              const bool cleaned = v_partly();
+              ready = cleaned ? mbar_test(bar(kGaVReady), v_cleaned & 1) : mbar_test(bar(kGaVFull), (v_gt - v_cleaned) & 1);
+              if (ready && cleaned) ++v_cleaned;
+            }
+          } else {
+            if (ready && v_grp == 0) ready = mbar_test(bar(kGaVFull), v_gt & 1);
+          }
           if (ready) {
             tc_fence_after();
             GA_TRACE(v_gt, 12 + v_grp);
@@ -292,7 +335,14 @@ __global__ void __launch_bounds__(kGaThreads, 1)
                 v_j = 0;
                 v_w = work_of(++v_r);
                 v_done = v_w >= p.num_work;
-                if (!v_done) item_of(v_w, b_, g_, p0_, v_T);
+                if (!v_done) {
+                  item_of(v_w, b_, g_, p0_, v_T);
+                  if constexpr (WIN) {
+                    v_p0 = p0_;
+                    v_nft = nft;
+                    v_t0 = t0;
+                  }
+                }
               }
             } else {
               v_grp = 1;
@@ -335,7 +385,7 @@ __global__ void __launch_bounds__(kGaThreads, 1)
         sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &os[k], &oc[k]);
       }
     }
-    int it = 0, gt = 0;
+    int it = 0, gt = 0, looked = 0;
     bool ok = true;
     for (int rd = 0, w = work_of(0); w < p.num_work && ok; w = work_of(++rd), ++it) {
       int b, g, p0, T;
@@ -353,7 +403,15 @@ __global__ void __launch_bounds__(kGaThreads, 1)
       mbar_arrive(bar(kGaQReady));
       for (int j = 0; j < T; ++j, ++gt) {
         const int ks = gt & 1;
-        const int kt0 = j * kGaBN;
+        const int kt0 = tile_of(j, nft, t0) * kGaBN;
+        // (WIN) the V row of this thread's key, from memory (the tile arrives later): if it is not
+        // finite the key's K row gets a NaN and the V row becomes zeros
+        bool look = false, v_bad = false;
+        if constexpr (WIN) {
+          look = partly(kt0, p.q_off + p0, p.q_off + p0 + 2 * P - 1);
+          if (look && kt0 + ctid < p.nk)
+            v_bad = v_row_not_finite(p.v + ((static_cast<long long>(b) * p.nk + kt0 + ctid) * p.Hkv + g) * 128);
+        }
         if (half > 0) {
           // base (cos, sin)(kt0 w_k) of this tile, by the first warp. Four buffers: a warp
           // that writes the table of tile t has seen K tile t-1 land, which needs every
@@ -419,8 +477,28 @@ __global__ void __launch_bounds__(kGaThreads, 1)
         } else {
           if (!wait_all(bar(kGaKFull + ks), (gt >> 1) & 1)) { ok = false; break; }
         }
+        if constexpr (WIN) {
+          if (v_bad) {   // dim 64 (the rotated dims are below it)
+            *reinterpret_cast<uint16_t*>(smem + L::OFF_K + ks * L::K_TILE + L::K_CHUNK + ctid * 128 + ((ctid & 7) << 4)) = kNan16;
+            fence_proxy_async_smem();
+          }
+        }
         mbar_arrive(bar(kGaKReady + ks));
         if (ctid == 0) GA_TRACE(gt, 9);
+        if constexpr (WIN) {
+          // S of the next tile needs this tile's PV, so its K can wait for this tile's V
+          if (look) {
+            if (!wait_all(bar(kGaVLook), looked & 1)) { ok = false; break; }
+            ++looked;
+            if (v_bad) {
+              for (int u = 0; u < 16; ++u)
+                *reinterpret_cast<uint4*>(smem + L::OFF_V + (u >> 3) * L::K_CHUNK + ctid * 128 + (u & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+            }
+            mbar_arrive(bar(kGaVReady));
+          }
+        }
       }
     }
   } else {
@@ -450,8 +528,9 @@ __global__ void __launch_bounds__(kGaThreads, 1)
         if (!wait_all(bar(kGaSFull + grp), gt & 1)) { ok = false; break; }
         tc_fence_after();
         if (q4 == 0 && lane == 0) GA_TRACE(gt, 4 + grp);
-        const int kt0 = j * kGaBN;
-        const bool full = kt0 + kGaBN - 1 <= pmin;   // every key of the tile is <= every row's pos
+        const int kt0 = tile_of(j, nft, t0) * kGaBN;
+        // every key of the tile is valid for every row (<= every row's pos, inside every window)
+        const bool full = WIN ? !partly(kt0, pmin, pmin + P - 1) : kt0 + kGaBN - 1 <= pmin;
         // pass 1: tile max of the valid keys, 64 columns per TMEM round trip
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
@@ -470,10 +549,11 @@ __global__ void __launch_bounds__(kGaThreads, 1)
             }
           } else {
             const int lim = pos - kt0 - c;   // columns e <= lim are keys <= pos
+            const int elo = lim - p.window + 1, ef = p.n_first - kt0 - c;   // (WIN) from elo on, or below ef
 #pragma unroll
             for (int e = 0; e < 64; e += 2) {
-              if (e <= lim) mx0 = fmaxf(mx0, __uint_as_float(v[e]));
-              if (e + 1 <= lim) mx1 = fmaxf(mx1, __uint_as_float(v[e + 1]));
+              if (e <= lim && (!WIN || e >= elo || e < ef)) mx0 = fmaxf(mx0, __uint_as_float(v[e]));
+              if (e + 1 <= lim && (!WIN || e + 1 >= elo || e + 1 < ef)) mx1 = fmaxf(mx1, __uint_as_float(v[e + 1]));
             }
           }
         }
@@ -517,6 +597,7 @@ __global__ void __launch_bounds__(kGaThreads, 1)
             reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(v));
             reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
             const int lim = pos - kt0 - c;   // columns e <= lim are keys <= pos
+            const int elo = lim - p.window + 1, ef = p.n_first - kt0 - c;   // (WIN) from elo on, or below ef
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t pk[8];
@@ -527,8 +608,8 @@ __global__ void __launch_bounds__(kGaThreads, 1)
                 float a0 = ex2(y.x);
                 float a1 = ex2(y.y);
                 if (decltype(masked)::value) {
-                  a0 = col <= lim ? a0 : 0.f;
-                  a1 = col + 1 <= lim ? a1 : 0.f;
+                  a0 = col <= lim && (!WIN || col >= elo || col < ef) ? a0 : 0.f;
+                  a1 = col + 1 <= lim && (!WIN || col + 1 >= elo || col + 1 < ef) ? a1 : 0.f;
                 }
                 sab = f2_add(sab, f2_pack(a0, a1));
                 pk[e] = pack_bf16(a0, a1);

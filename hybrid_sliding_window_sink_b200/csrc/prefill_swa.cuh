@@ -34,6 +34,11 @@
 // Each softmax group owns 256 TMEM columns: S in [0, 176), overwritten in place by P
 // (f16, two keys per column) in [0, 88), and O in [128, 256) (S is dead by then). The
 // PV MMA takes A = P from TMEM and B = V from the ring.
+// FIRST: the first n_first <= 16 tokens stay visible. They sit in one more unit behind the ring,
+// loaded once per (sequence, KV head) run: S has 192 columns, P lies in [0, 96). A key below a
+// row's window counts through that unit, one inside it through the ring, so none counts twice.
+// Every tile masks keys, so V rows that hold a NaN become zeros and their K rows NaN as they enter
+// (see v_row_not_finite in prefill.cuh; infinities are clamped).
 // Precision: rotated Q/K dims are stored as f16 and their QK^T k-steps run as f16 MMAs
 // (see prefill.cuh); P and V are f16 too (each V unit is converted in place once when it
 // enters the ring; P in [0, 1] keeps 11 significant bits instead of 8). P is scaled by the
@@ -63,14 +68,16 @@ constexpr int kSwaThreads = 448;
 constexpr int kSwaG = 8;            // query heads per KV head
 constexpr int kSwaP = 16;           // positions per row block
 constexpr int kSwaUnits = 11;       // 16-row units in the ring
-constexpr int kSwaR = 16 * kSwaUnits;
 constexpr int kSwaWin = 9;          // units holding the 144-key span of a row block
-constexpr int kSwaN = kSwaR;        // S columns: the whole ring, in slot order
+constexpr int kSwaFirst = 16;       // most first tokens (one unit)
 
+template <bool FIRST>
 struct SwaLayout {
+  static constexpr int UNITS = kSwaUnits + (FIRST ? 1 : 0);   // the ring, and the first tokens
+  static constexpr int N = 16 * UNITS;                 // S columns: all units, in slot order
   static constexpr int Q_CHUNK = 128 * 128;
   static constexpr int Q_STAGE = 3 * Q_CHUNK;
-  static constexpr int R_CHUNK = kSwaR * 128;          // 176 rows x 64 dims
+  static constexpr int R_CHUNK = N * 128;              // 176 (192) rows x 64 dims
   static constexpr int UNIT_BYTES = 16 * 128;          // one unit inside one 64-dim chunk
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + 2 * Q_STAGE;
@@ -81,8 +88,8 @@ struct SwaLayout {
   static constexpr int MISC_BYTES = 512 + 32 * 8;
   static constexpr int SMEM = OFF_MISC + MISC_BYTES + 1024;
   static constexpr uint32_t IDESC_PV = idesc_f16kind(128, 128, 0, 1, 1);   // P and V in f16
-  static constexpr uint32_t IDESC_S = idesc_bf16(128, kSwaN, 0, 0);
-  static constexpr uint32_t IDESC_S_F16 = idesc_f16kind(128, kSwaN, 0, 0, 1);   // rotated dims
+  static constexpr uint32_t IDESC_S = idesc_bf16(128, N, 0, 0);
+  static constexpr uint32_t IDESC_S_F16 = idesc_f16kind(128, N, 0, 0, 1);   // rotated dims
   static_assert(R_CHUNK % 1024 == 0, "ring chunks stay on swizzle atoms");
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -100,7 +107,10 @@ enum : int {
   kSwKVFull = 17,    // [11] unit landed
   kSwKReady = 28,    // [11] unit rotated (128 arrivals)
   kSwSlotFree = 39,  // [11] last MMA reading the unit finished
-  kSwNumBars = 50
+  kSwFirstFull = 50,  // (FIRST) the first tokens' unit: landed, rotated (128 arrivals), free again
+  kSwFirstReady = 51,
+  kSwFirstFree = 52,
+  kSwNumBars = 53
 };
 
 // (x, y) <- (x cos - y sin, y cos + x sin) for two rotation pairs: xw and yw each hold two
@@ -173,10 +183,11 @@ __device__ __forceinline__ void rope_row_tab(uint8_t* row_base, int row, int nun
   rope_half(row_base, row, nun, t4, 2);
 }
 
+template <bool FIRST>
 __global__ void __launch_bounds__(kSwaThreads, 1)
     prefill_swa_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const PrefillParams p) {
-  using L = SwaLayout;
+  using L = SwaLayout<FIRST>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -197,7 +208,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
     for (int i = 0; i < kSwNumBars; ++i) {
       const bool many = (i >= kSwQReady && i < kSwQReady + 2) || (i >= kSwPReady && i < kSwPReady + 2) ||
                         (i >= kSwTmFree && i < kSwTab + 2) ||
-                        (i >= kSwKReady && i < kSwKReady + kSwaUnits);
+                        (i >= kSwKReady && i < kSwKReady + kSwaUnits) || i == kSwFirstReady;
       mbar_init(bar(i), many ? 128u : 1u);
     }
     *s_abort = 0;
@@ -232,7 +243,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int seq = 0, nq = 0;
+      int seq = 0, nq = 0, nfirst = 0;
       bool ok = true;
       auto load_unit = [&](int b, int g, int u) -> bool {
         const int slot = seq % kSwaUnits;
@@ -255,6 +266,19 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         const int ua = t + (p.q_off >> 4);   // K/V unit holding the block's own positions
         if (f == f0 || t == 0)
           for (int u = ua - 8; u < ua && ok; ++u) ok = load_unit(b, g, u);
+        if constexpr (FIRST) {
+          if (ok && (f == f0 || t == 0)) {   // keys 0 .. 15 of this sequence and KV head
+            if (nfirst > 0) ok = mbar_wait(bar(kSwFirstFree), (nfirst - 1) & 1, s_abort, err);
+            if (ok) {
+              mbar_arrive_expect_tx(bar(kSwFirstFull), 16 * (kDQK + kDV) * 2);
+              for (int c = 0; c < 3; ++c)
+                tma_load_4d(sK + c * L::R_CHUNK + kSwaUnits * L::UNIT_BYTES, &tmK, bar(kSwFirstFull), 64 * c, g, 0, b);
+              for (int c = 0; c < 2; ++c)
+                tma_load_4d(sV + c * L::R_CHUNK + kSwaUnits * L::UNIT_BYTES, &tmV, bar(kSwFirstFull), 64 * c, g, 0, b);
+              ++nfirst;
+            }
+          }
+        }
         if (!ok) break;
         const int st = nq & 1;
         if (nq >= 2 && !mbar_wait(bar(kSwQEmpty + st), ((nq >> 1) - 1) & 1, s_abort, err)) { ok = false; break; }
@@ -271,6 +295,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
           mbar_wait_drain(bar(kSwKVFull + s % kSwaUnits), (s / kSwaUnits) & 1, err);
         for (int i = nq - 2 < 0 ? 0 : nq - 2; i < nq; ++i)
           mbar_wait_drain(bar(kSwQFull + (i & 1)), (i >> 1) & 1, err);
+        if (FIRST && nfirst > 0) mbar_wait_drain(bar(kSwFirstFull), (nfirst - 1) & 1, err);
       }
     }
   } else if (warp == 1) {
@@ -282,6 +307,8 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       bool last_of[4] = {false, false, false, false};
       int s_useq = 0, kwait = 0;
       bool s_last = false, s_q = false, s_free = false, ok = true;
+      bool s_first = !FIRST;                   // the run's first tokens are in place
+      int runs = 0;
       auto prep_s = [&]() {
         const long long f = f0 + ns;
         const int t = static_cast<int>(f % nqt);
@@ -292,6 +319,10 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         kwait = first ? s_useq - 8 : s_useq;
         s_q = false;
         s_free = ns < 2;
+        if (FIRST && first) {
+          s_first = false;
+          ++runs;
+        }
       };
       if (ntiles > 0) prep_s();
       unsigned long long t_prog = globaltimer_ns();
@@ -305,7 +336,8 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
           while (s_q && kwait <= s_useq &&
                  mbar_test(bar(kSwKReady + kwait % kSwaUnits), (kwait / kSwaUnits) & 1))
             ++kwait;
-          if (s_q && s_free && kwait > s_useq) {
+          if (!s_first) s_first = mbar_test(bar(kSwFirstReady), (runs - 1) & 1);
+          if (s_q && s_free && s_first && kwait > s_useq) {
             SWA_TRACE(ns, 17);
             tc_fence_after();
             const uint32_t d = tmem + wg * 256;
@@ -334,15 +366,26 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
             const int uq = useq_of[npv & 3];
             const uint32_t base = tmem + wg * 256;
 #pragma unroll
-            for (int s2 = 0; s2 < kSwaUnits; ++s2) {
+            for (int s2 = 0; s2 < L::UNITS; ++s2) {
               const uint64_t bd = smem_desc(sV + s2 * L::UNIT_BYTES, L::R_CHUNK, 1024);
-              umma_ts(base + 128, base + 8 * s2, bd, L::IDESC_PV, s2 > 0 ? 1u : 0u);
+              if constexpr (FIRST) {
+                // not the two slots outside the window: they may be taking rows of later keys, which
+                // are not f16 yet (and may hold anything). The first unit is always in, and first.
+                const int u2 = s2 == 0 ? kSwaUnits : s2 - 1;
+                const int back = uq % kSwaUnits - u2;
+                if (s2 > 0 && (back < 0 ? back + kSwaUnits : back) >= kSwaWin) continue;
+                umma_ts(base + 128, base + 8 * u2, smem_desc(sV + u2 * L::UNIT_BYTES, L::R_CHUNK, 1024), L::IDESC_PV,
+                        s2 > 0 ? 1u : 0u);
+              } else {
+                umma_ts(base + 128, base + 8 * s2, bd, L::IDESC_PV, s2 > 0 ? 1u : 0u);
+              }
             }
             umma_commit(bar(kSwPVDone + wg));
             umma_commit(bar(kSwSlotFree + (uq - 8) % kSwaUnits));
             if (last_of[npv & 3])
               for (int s2 = 1; s2 < kSwaWin; ++s2)
                 umma_commit(bar(kSwSlotFree + (uq - 8 + s2) % kSwaUnits));
+            if (FIRST && last_of[npv & 3]) umma_commit(bar(kSwFirstFree));
             SWA_TRACE(npv, 8);
             ++npv;
             prog = true;
@@ -372,7 +415,41 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       const bool w_ok = mbar_wait(b_, par, s_abort, err);
       return __all_sync(0xffffffffu, w_ok);
     };
-    int seq = 0, i = 0;
+    // V rows of a unit (slot) of the ring: bf16 -> f16 in place; (FIRST) a NaN becomes 0 and a NaN
+    // in the key's K row, at dim 64 (the rotated dims are below it)
+    auto v_unit = [&](int slot) {
+      uint8_t* vb = smem + L::OFF_V + slot * L::UNIT_BYTES;
+      uint4 xv[2];
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2)
+        xv[h2] = *reinterpret_cast<const uint4*>(vb + h2 * L::R_CHUNK + ctid * 16);
+      if constexpr (FIRST) {
+        bool bad = false;
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) {
+          uint32_t w[4] = {xv[h2].x, xv[h2].y, xv[h2].z, xv[h2].w};
+          bool nan = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
+            nan |= !__hbeq2(x, x);
+          }
+          if (nan) {
+            xv[h2] = make_uint4(0u, 0u, 0u, 0u);
+            bad = true;
+          }
+        }
+        const int row = ctid >> 3;
+        if (bad)
+          *reinterpret_cast<uint16_t*>(smem + L::OFF_K + L::R_CHUNK + slot * L::UNIT_BYTES + row * 128 + ((row & 7) << 4)) = kNan16;
+      }
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2)
+        *reinterpret_cast<uint4*>(vb + h2 * L::R_CHUNK + ctid * 16) =
+            make_uint4(bf16x2_to_f16x2(xv[h2].x), bf16x2_to_f16x2(xv[h2].y),
+                       bf16x2_to_f16x2(xv[h2].z), bf16x2_to_f16x2(xv[h2].w));
+    };
+    int seq = 0, i = 0, runs = 0;
     for (long long f = f0; f < f1; ++f, ++i) {
       const int t = static_cast<int>(f % nqt);
       const bool first = (f == f0 || t == 0);
@@ -406,17 +483,20 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       const int s_first = first ? useq - 8 : useq;
       for (int s = s_first; s <= useq && ok; ++s) ok = wait_all(bar(kSwKVFull + s % kSwaUnits), (s / kSwaUnits) & 1);
       if (!ok) break;
-      for (int s = s_first; s <= useq; ++s) {   // V units entering the ring: bf16 -> f16 in place
-        uint8_t* vb = smem + L::OFF_V + (s % kSwaUnits) * L::UNIT_BYTES;
-        uint4 xv[2];
-#pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2)
-          xv[h2] = *reinterpret_cast<const uint4*>(vb + h2 * L::R_CHUNK + ctid * 16);
-#pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2)
-          *reinterpret_cast<uint4*>(vb + h2 * L::R_CHUNK + ctid * 16) =
-              make_uint4(bf16x2_to_f16x2(xv[h2].x), bf16x2_to_f16x2(xv[h2].y),
-                         bf16x2_to_f16x2(xv[h2].z), bf16x2_to_f16x2(xv[h2].w));
+      for (int s = s_first; s <= useq; ++s) v_unit(s % kSwaUnits);   // V units entering the ring
+      if constexpr (FIRST) {
+        if (first) {                                 // and the first tokens' unit of a new run
+          if (!wait_all(bar(kSwFirstFull), runs & 1)) break;
+          v_unit(kSwaUnits);
+          if (half > 0 && ctid < 16) {
+            const int ring_row = kSwaUnits * 16 + ctid;
+            if (ctid >= p.krot_from && ctid < p.nk) rope_row(sK, L::R_CHUNK, ring_row, ctid, p.rot_dims, s_invf);
+            else if (ctid < p.krot_from) f16_row(sK, L::R_CHUNK, ring_row, p.rot_dims);
+          }
+          ++runs;
+          fence_proxy_async_smem();
+          mbar_arrive(bar(kSwFirstReady));
+        }
       }
       if (half > 0) {
         if (first) {
@@ -476,6 +556,11 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       const int um = useq % kSwaUnits;
       // 0 = empty, 1 = partial, 2 = full; elo/ehi: valid e of this row (partial blocks)
       auto block_class = [&](int c, int& elo, int& ehi) -> int {
+        if (FIRST && c == kSwaUnits) {   // first tokens below this row's window
+          elo = 0;
+          ehi = min(p.n_first, klo) - 1;
+          return min(p.n_first, klo_max) <= 0 ? 0 : (min(p.n_first, klo_min) >= 16 ? 2 : 1);
+        }
         int d = um - c;
         d += d < 0 ? kSwaUnits : 0;
         const int kb = p0 - 16 * d;
@@ -490,12 +575,12 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       // pass 1: row max over the valid keys (four slot blocks per TMEM round trip)
       float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
-      for (int c = 0; c < kSwaUnits; c += 2) {
+      for (int c = 0; c < L::UNITS; c += 2) {
         uint32_t v[2][16];
         int elo[2], ehi[2], k[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          k[q] = c + q < kSwaUnits ? block_class(c + q, elo[q], ehi[q]) : 0;
+          k[q] = c + q < L::UNITS ? block_class(c + q, elo[q], ehi[q]) : 0;
           if (k[q]) tmem_ld16(trow + (c + q) * 16, v[q]);
         }
         tmem_wait_ld();
@@ -548,18 +633,18 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         return sab.x + sab.y;
       };
 #pragma unroll 1
-      for (int c = 0; c < kSwaUnits; c += 2) {
+      for (int c = 0; c < L::UNITS; c += 2) {
         uint32_t v[2][16];
         int elo[2], ehi[2], k[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          k[q] = c + q < kSwaUnits ? block_class(c + q, elo[q], ehi[q]) : 0;
+          k[q] = c + q < L::UNITS ? block_class(c + q, elo[q], ehi[q]) : 0;
           if (k[q]) tmem_ld16(trow + (c + q) * 16, v[q]);
         }
         tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          if (c + q < kSwaUnits) {
+          if (c + q < L::UNITS) {
             uint32_t pk[8];
             const float sq = p_block(v[q], k[q], elo[q], ehi[q], pk);
             if (q & 1) sum1 += sq; else sum0 += sq;

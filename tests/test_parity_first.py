@@ -149,3 +149,39 @@ def test_repeats_streams_graph(cuda_device):
         torch.cuda.synchronize()
         for got in (other, (out, lse), call()):
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,window,first", [(8, 1, 128, 4), (8, 1, 200, 40), (16, 1, 64, 130), (4, 2, 128, 4)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_that_are_not_finite_stay_where_they_are_seen(cuda_device, hq, hkv, window, first, bad):
+    """A V row of NaN or infinity: queries that mask its key are as if it were 0 (a weight of 0 must
+    not multiply it), queries that see a NaN are NaN (the column, or the whole row). Also K rows that are not finite behind a
+    sequence's end, as the padding of a batch may hold them."""
+    n = 400
+    inp = _inputs(1, n, 0, hq, hkv, 70)
+    clean = {k: v.clone() for k, v in inp.items()}
+    at = [2, 150, 333]
+    for t in at:
+        inp["v"][0, t, 0, t % 128] = bad
+        clean["v"][0, t, 0] = 0
+    inp["k"][0, 385:] = bad
+    inp["v"][0, 385:] = bad
+    d = {k: v.to(cuda_device) for k, v in inp.items()}
+    out, lse = _lib.prefill_first(d["q"], d["k"], d["v"], d["sink"], window=window, n_first=first)
+    torch.cuda.synchronize()
+    assert _lib.last_device_error() == 0
+    o, l, mass = serve.prefill_first(*(wl.to_f64(clean[x]) for x in "qkv"), 0, False, wl.to_f64(inp["sink"]), window,
+                                     first, 1e4, 64)
+    seen = np.array([[any(t <= i and (t > i - window or t < first) for t in at) for i in range(n)]])
+    seen = np.repeat(seen[..., None], hq, -1)
+    seen[:, :, hq // hkv:] = False                       # the other KV heads are clean
+    seen[:, 385:] = True
+    fine = ~seen
+    got = wl.to_f64(out)
+    tol = np.abs(o) * BF16 + mass * (BF16 + 2 * _delta(clean, 64))
+    assert (np.abs(got - o)[fine] <= tol[fine]).all()
+    if bad != bad:                                       # the definition's NaN: that column of the rows that see it
+        for t in at:
+            sees = [i for i in range(t, 385) if t > i - window or t < first]
+            assert np.isnan(got[0, sees, :hq // hkv, t % 128]).all()
