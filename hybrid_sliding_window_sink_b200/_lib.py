@@ -10,6 +10,7 @@ arithmetic happens in the library's CUDA kernels. The library must be built
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -427,47 +428,55 @@ def sparse(q, k_cache, v_cache, lengths, sel_idx, sink=None, *, recent=128, capa
     return out, lse
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream   # of a device index, without a Stream object
+
+
 class _On:
-    """Makes the tensors' device current and yields the raw stream to launch on: the given
-    stream (which must belong to that device), or the device's current one. Scratch and outputs
-    allocated inside belong to that stream."""
+    """Makes device ``index`` current and yields the raw stream to launch on: the given stream
+    (which must belong to that device), or the device's current one. Scratch and outputs
+    allocated inside belong to that stream. Not used where the device is current already and no
+    stream is given (the usual call, see _usual)."""
 
-    __slots__ = ("ctx", "stream")
+    __slots__ = ("ctx", "index")
 
-    def __init__(self, device, stream):
-        self.ctx = None
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream of {stream.device} for tensors on {device}")
-            self.ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
-        self.stream = stream
+    def __init__(self, index, stream):
+        self.index = index
+        if stream is not None and stream.device_index != index:
+            raise ValueError(f"stream of device {stream.device_index} for tensors on device {index}")
+        self.ctx = torch.cuda.device(index) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream()
-        return s.cuda_stream
+        self.ctx.__enter__()
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        return self.ctx.__exit__(*exc)
+
+
+def _usual(index, stream):
+    return stream is None and index == torch.cuda.current_device()
 
 
 def _need_at(t, name, dtype, shape, device, contiguous=True):
     """t is a tensor of that dtype, shape (None: any size) and device."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device:
+        have = t.shape
+        if have == shape or _fits(have, shape):
+            if not contiguous or t.is_contiguous():
+                return
+            raise ValueError(f"{name} must be contiguous")
+        want = tuple("*" if n is None else n for n in shape)
+        raise ValueError(f"{name} must have shape {want}, got {tuple(have)}")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    have = t.shape
-    if len(have) != len(shape) or any(n is not None and n != h for n, h in zip(shape, have)):
-        raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, got {tuple(have)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+@functools.lru_cache(maxsize=1024)
+def _fits(have, shape):
+    return len(have) == len(shape) and all(n is None or n == h for n, h in zip(shape, have))
 
 
 def _cuda_device(t, name):
@@ -485,7 +494,7 @@ def prefill_first(q, k, v, sink=None, *, window, n_first, pos_offset=0, k_prefix
     ``n_first``. Returns (out [B,n,Hq,128] bf16, lse [B,Hq,n] fp32 or None)."""
     dev = _cuda_device(q, "q")
     _need_at(q, "q", torch.bfloat16, (None, None, None, 192), dev)
-    B, n, hq = q.shape[:3]
+    B, n, hq, _ = q.shape
     _need_at(k, "k", torch.bfloat16, (B, pos_offset + n, None, 192), dev)
     hkv = k.shape[2]
     _need_at(v, "v", torch.bfloat16, (B, pos_offset + n, hkv, 128), dev)
@@ -495,88 +504,123 @@ def prefill_first(q, k, v, sink=None, *, window, n_first, pos_offset=0, k_prefix
         _need_at(out, "out", torch.bfloat16, (B, n, hq, 128), dev)
     if lse is not None:
         _need_at(lse, "lse", torch.float32, (B, hq, n), dev)
-    shape = MimoShape(B, n, hq, hkv, 192, 128, float(softmax_scale))
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty(B, n, hq, 128, dtype=torch.bfloat16, device=dev)
-        if lse is None and want_lse:
-            lse = torch.empty(B, hq, n, dtype=torch.float32, device=dev)
-        rc = lib().mimo_attn_prefill_first(shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), int(pos_offset),
-                                           1 if k_prefix_rotated else 0, _addr(sink), int(window), int(n_first),
-                                           float(rope_theta), int(rot_dims), out.data_ptr(), _addr(lse), st)
-    _check("mimo_attn_prefill_first", rc)
-    return out, lse
+
+    def launch(st):
+        o = torch.empty((B, n, hq, 128), dtype=torch.bfloat16, device=dev) if out is None else out
+        ls = torch.empty((B, hq, n), dtype=torch.float32, device=dev) if lse is None and want_lse else lse
+        _check("mimo_attn_prefill_first", lib().mimo_attn_prefill_first(
+            _shape_struct(B, n, hq, hkv, softmax_scale), q.data_ptr(), k.data_ptr(), v.data_ptr(), pos_offset,
+            1 if k_prefix_rotated else 0, _addr(sink), window, n_first, rope_theta, rot_dims, o.data_ptr(), _addr(ls), st))
+        return o, ls
+
+    if _usual(dev.index, stream):
+        return launch(_raw_stream(dev.index))
+    with _On(dev.index, stream) as st:
+        return launch(st)
 
 
-def _pages(k, v, table, scales=()):
-    """mimo_pages of the pools k [num_pages, page_size, Hkv, 192], v [.., 128] and the scales
-    [num_pages, page_size, Hkv]: each contiguous within a page, with the same distance between
-    pages, in whole tokens."""
-    n, page, hkv = k.shape[:3]
-    if n < 1 or page < 1 or hkv < 1:
+def _pool_stride(shape, strides, name):
+    """Tokens between the pages of a pool [num_pages, page_size, Hkv(, D)] that is contiguous
+    within a page."""
+    if shape[0] < 1 or shape[1] < 1 or shape[2] < 1:
         raise ValueError("the pool holds no page")
-    stride = None
-    for name, t in (("k_pages", k), ("v_pages", v), *scales):
-        row = hkv * t.shape[3] if t.dim() == 4 else hkv
-        inner = (row, t.shape[3], 1) if t.dim() == 4 else (row, 1)
-        if any(s != w and d > 1 for s, w, d in zip(t.stride()[1:], inner, t.shape[1:])):
-            raise ValueError(f"{name} must be contiguous within a page")
-        step = t.stride(0) if n > 1 else page * row
-        if step % row or step < page * row:
-            raise ValueError(f"{name}: pages must not overlap and must lie whole tokens apart")
-        if stride is not None and step // row != stride:
+    row = shape[2] * shape[3] if len(shape) == 4 else shape[2]
+    inner = (row, shape[3], 1) if len(shape) == 4 else (row, 1)
+    if strides[1:] != inner and any(s != w and d > 1 for s, w, d in zip(strides[1:], inner, shape[1:])):
+        raise ValueError(f"{name} must be contiguous within a page")
+    if shape[0] == 1:
+        return shape[1]
+    if strides[0] % row or strides[0] < shape[1] * row:
+        raise ValueError(f"{name}: pages must not overlap and must lie whole tokens apart")
+    return strides[0] // row
+
+
+@functools.lru_cache(maxsize=1024)
+def _pools_stride(kshape, kstrides, *rest):
+    """Tokens between pages of pools of these shapes and strides (K, V, scales), the same in all."""
+    stride = _pool_stride(kshape, kstrides, "k_pages")
+    for name, shape, strides in zip(("v_pages", "k_scale", "v_scale"), rest[::2], rest[1::2]):
+        if _pool_stride(shape, strides, name) != stride:
             raise ValueError("K, V and scale pools must have the same distance between pages")
-        stride = step // row
-    return MimoPages(table.data_ptr(), table.shape[1], n, page, stride)
+    return stride
+
+
+def _pages(k, v, table, scales=None):
+    """mimo_pages of the pools k [num_pages, page_size, Hkv, 192], v [.., 128] and the scales
+    [num_pages, page_size, Hkv]."""
+    ks = k.shape
+    if scales is None:
+        stride = _pools_stride(ks, k.stride(), v.shape, v.stride())
+    else:
+        a, b = scales
+        stride = _pools_stride(ks, k.stride(), v.shape, v.stride(), a.shape, a.stride(), b.shape, b.stride())
+    return MimoPages(table.data_ptr(), table.shape[1], ks[0], ks[1], stride)
+
+
+def _need_pools(k, v, scales, hkv, dev):
+    """Checks the pools of one call."""
+    dt = torch.bfloat16 if scales is None else torch.uint8
+    _need_at(k, "k_pages", dt, (None, None, hkv, 192), dev, contiguous=False)
+    n, page, hkv, _ = k.shape
+    _need_at(v, "v_pages", dt, (n, page, hkv, 128), dev, contiguous=False)
+    if scales is not None:
+        _need_at(scales[0], "k_scale", torch.float32, (n, page, hkv), dev, contiguous=False)
+        _need_at(scales[1], "v_scale", torch.float32, (n, page, hkv), dev, contiguous=False)
+
+
+@functools.lru_cache(maxsize=1024)
+def _shape_struct(batch, seqlen, hq, hkv, softmax_scale):
+    """mimo_shape of these sizes (only ever read)."""
+    return MimoShape(batch, seqlen, hq, hkv, 192, 128, softmax_scale)
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_workspace(index, batch, hq, hkv, max_pages, page_size, window, n_first):
+    """Workspace bytes by sizes (and the device, which is current)."""
+    return int(lib().mimo_attn_decode_paged_workspace_size(
+        make_shape(batch, 1, hq, hkv), MimoPages(None, max_pages, 1, page_size, page_size), window, n_first))
 
 
 def _decode_paged(q, k, v, scales, table, lengths, sink, window, n_first, softmax_scale, out, lse, want_lse,
                   workspace, stream):
     dev = _cuda_device(q, "q")
-    fp8 = scales is not None
     _need_at(q, "q", torch.bfloat16, (None, None, 192), dev)
-    B, hq = q.shape[:2]
-    dt = torch.uint8 if fp8 else torch.bfloat16
-    _need_at(k, "k_pages", dt, (None, None, None, 192), dev, contiguous=False)
-    n, page, hkv = k.shape[:3]
-    _need_at(v, "v_pages", dt, (n, page, hkv, 128), dev, contiguous=False)
+    B, hq, _ = q.shape
+    _need_pools(k, v, scales, None, dev)
     _need_at(table, "block_table", torch.int32, (B, None), dev)
     _need_at(lengths, "lengths", torch.int32, (B,), dev)
-    named = ()
-    if fp8:
-        named = (("k_scale", scales[0]), ("v_scale", scales[1]))
-        for name, t in named:
-            _need_at(t, name, torch.float32, (n, page, hkv), dev, contiguous=False)
     if sink is not None:
         _need_at(sink, "sink", torch.float32, (hq,), dev)
     if out is not None:
         _need_at(out, "out", torch.bfloat16, (B, hq, 128), dev)
     if lse is not None:
         _need_at(lse, "lse", torch.float32, (B, hq), dev)
-    pages = _pages(k, v, table, named)
-    shape = MimoShape(B, 1, hq, hkv, 192, 128, float(softmax_scale))
-    L = lib()
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty(B, hq, 128, dtype=torch.bfloat16, device=dev)
-        if lse is None and want_lse:
-            lse = torch.empty(B, hq, dtype=torch.float32, device=dev)
-        nbytes = L.mimo_attn_decode_paged_workspace_size(shape, pages, int(window), int(n_first))
-        if workspace is not None:
-            _cuda_device(workspace, "workspace")
-            if workspace.device != dev or not workspace.is_contiguous():
-                raise ValueError(f"workspace must be contiguous and on {dev}")
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or workspace.device != dev
+                                  or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    pages = _pages(k, v, table, scales)
+    hkv = k.shape[2]
+
+    def launch(st):
+        o = torch.empty((B, hq, 128), dtype=torch.bfloat16, device=dev) if out is None else out
+        ls = torch.empty((B, hq), dtype=torch.float32, device=dev) if lse is None and want_lse else lse
+        nbytes = _paged_workspace(dev.index, B, hq, hkv, pages.max_pages, pages.page_size, window, n_first)
         ws = _workspace(workspace, nbytes, dev)
-        tail = (_addr(sink), out.data_ptr(), _addr(lse), _addr(ws), nbytes, st)
-        if fp8:
-            rc = L.mimo_attn_decode_paged_fp8(shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), scales[0].data_ptr(),
-                                              scales[1].data_ptr(), pages, lengths.data_ptr(), int(window),
-                                              int(n_first), *tail)
+        shape = _shape_struct(B, 1, hq, hkv, softmax_scale)
+        if scales is None:
+            _check("mimo_attn_decode_paged", lib().mimo_attn_decode_paged(
+                shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), pages, lengths.data_ptr(), window, n_first,
+                _addr(sink), o.data_ptr(), _addr(ls), _addr(ws), nbytes, st))
         else:
-            rc = L.mimo_attn_decode_paged(shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), pages,
-                                          lengths.data_ptr(), int(window), int(n_first), *tail)
-    _check("mimo_attn_decode_paged_fp8" if fp8 else "mimo_attn_decode_paged", rc)
-    return out, lse
+            _check("mimo_attn_decode_paged_fp8", lib().mimo_attn_decode_paged_fp8(
+                shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), scales[0].data_ptr(), scales[1].data_ptr(), pages,
+                lengths.data_ptr(), window, n_first, _addr(sink), o.data_ptr(), _addr(ls), _addr(ws), nbytes, st))
+        return o, ls
+
+    if _usual(dev.index, stream):
+        return launch(_raw_stream(dev.index))
+    with _On(dev.index, stream) as st:
+        return launch(st)
 
 
 def decode_paged(q, k_pages, v_pages, block_table, lengths, sink=None, *, window=0, n_first=0, softmax_scale=0.0,
@@ -599,40 +643,37 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, lengths
 
 def decode_paged_workspace_size(batch, hq, hkv, *, max_pages, page_size, window=0, n_first=0):
     """Bytes of workspace the paged decodes need on the current device."""
-    pages = MimoPages(None, int(max_pages), 1, int(page_size), int(page_size))
-    return int(lib().mimo_attn_decode_paged_workspace_size(make_shape(batch, 1, hq, hkv), pages, int(window),
-                                                           int(n_first)))
+    return _paged_workspace(torch.cuda.current_device(), batch, hq, hkv, max_pages, page_size, window, n_first)
 
 
 def _append_paged(k_new, v_new, k, v, scales, table, positions, n_new, rope_theta, rot_dims, stream):
     dev = _cuda_device(k_new, "k_new")
-    fp8 = scales is not None
     _need_at(k_new, "k_new", torch.bfloat16, (None, None, None, 192), dev)
-    B, n, hkv = k_new.shape[:3]
+    B, n, hkv, _ = k_new.shape
     _need_at(v_new, "v_new", torch.bfloat16, (B, n, hkv, 128), dev)
-    dt = torch.uint8 if fp8 else torch.bfloat16
-    _need_at(k, "k_pages", dt, (None, None, hkv, 192), dev, contiguous=False)
-    N, page = k.shape[:2]
-    _need_at(v, "v_pages", dt, (N, page, hkv, 128), dev, contiguous=False)
+    _need_pools(k, v, scales, hkv, dev)
     _need_at(table, "block_table", torch.int32, (B, None), dev)
     _need_at(positions, "positions", torch.int32, (B,), dev)
     if n_new is not None:
         _need_at(n_new, "n_new", torch.int32, (B,), dev)
-    named = ()
-    if fp8:
-        named = (("k_scale", scales[0]), ("v_scale", scales[1]))
-        for name, t in named:
-            _need_at(t, name, torch.float32, (N, page, hkv), dev, contiguous=False)
-    pages = _pages(k, v, table, named)
-    shape = MimoShape(B, n, hkv, hkv, 192, 128, 0.0)
-    with _On(dev, stream) as st:
-        head = (shape, k_new.data_ptr(), v_new.data_ptr(), positions.data_ptr(), _addr(n_new), float(rope_theta),
-                int(rot_dims), pages, k.data_ptr(), v.data_ptr())
-        if fp8:
-            rc = lib().mimo_attn_cache_append_paged_fp8(*head, scales[0].data_ptr(), scales[1].data_ptr(), st)
+    pages = _pages(k, v, table, scales)
+
+    def launch(st):
+        shape = _shape_struct(B, n, hkv, hkv, 0.0)
+        if scales is None:
+            _check("mimo_attn_cache_append_paged", lib().mimo_attn_cache_append_paged(
+                shape, k_new.data_ptr(), v_new.data_ptr(), positions.data_ptr(), _addr(n_new), rope_theta, rot_dims,
+                pages, k.data_ptr(), v.data_ptr(), st))
         else:
-            rc = lib().mimo_attn_cache_append_paged(*head, st)
-    _check("mimo_attn_cache_append_paged_fp8" if fp8 else "mimo_attn_cache_append_paged", rc)
+            _check("mimo_attn_cache_append_paged_fp8", lib().mimo_attn_cache_append_paged_fp8(
+                shape, k_new.data_ptr(), v_new.data_ptr(), positions.data_ptr(), _addr(n_new), rope_theta, rot_dims,
+                pages, k.data_ptr(), v.data_ptr(), scales[0].data_ptr(), scales[1].data_ptr(), st))
+
+    if _usual(dev.index, stream):
+        launch(_raw_stream(dev.index))
+    else:
+        with _On(dev.index, stream) as st:
+            launch(st)
 
 
 def cache_append_paged(k_new, v_new, k_pages, v_pages, block_table, positions, *, n_new=None, rope_theta=1e4,
@@ -675,17 +716,19 @@ def verify_drafts(target_probs, draft_tokens, uniforms, draft_probs=None, *, n_v
         _need_at(n_accepted, "n_accepted", torch.int32, (B,), dev)
     if tokens is not None:
         _need_at(tokens, "tokens", torch.int32, (B, T1), dev)
-    with _On(dev, stream) as st:
-        if n_accepted is None:
-            n_accepted = torch.empty(B, dtype=torch.int32, device=dev)
-        if tokens is None:
-            tokens = torch.empty(B, T1, dtype=torch.int32, device=dev)
-        rc = lib().mimo_attn_verify_drafts(B, T, V, 0 if target_probs.dtype == torch.float32 else 1,
-                                           target_probs.data_ptr(), _addr(draft_probs), draft_tokens.data_ptr(),
-                                           uniforms.data_ptr(), _addr(n_valid), n_accepted.data_ptr(),
-                                           tokens.data_ptr(), st)
-    _check("mimo_attn_verify_drafts", rc)
-    return n_accepted, tokens
+
+    def launch(st):
+        acc = torch.empty((B,), dtype=torch.int32, device=dev) if n_accepted is None else n_accepted
+        tok = torch.empty((B, T1), dtype=torch.int32, device=dev) if tokens is None else tokens
+        _check("mimo_attn_verify_drafts", lib().mimo_attn_verify_drafts(
+            B, T, V, 0 if target_probs.dtype == torch.float32 else 1, target_probs.data_ptr(), _addr(draft_probs),
+            draft_tokens.data_ptr(), uniforms.data_ptr(), _addr(n_valid), acc.data_ptr(), tok.data_ptr(), st))
+        return acc, tok
+
+    if _usual(dev.index, stream):
+        return launch(_raw_stream(dev.index))
+    with _On(dev.index, stream) as st:
+        return launch(st)
 
 
 def check_indices(lengths, sel_idx, *, hq, recent=128, capacity, stream=None):

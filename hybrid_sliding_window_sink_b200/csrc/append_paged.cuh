@@ -29,7 +29,7 @@ struct AppendPagedParams {
   const int* table;           // [B, max_pages]
   const int* pos;             // [B] position of the chunk's first token
   const int* n_new;           // [B] tokens to write (null: n)
-  long long page_stride;
+  int page_stride;
   int B, n, Hkv, rot, page_size, max_pages, num_pages, tokens;   // tokens: per CTA
   double invf[kDQK / 2];      // theta^(-2d/rot)
 };
@@ -48,14 +48,24 @@ __device__ __forceinline__ void unpack8(const uint4 x, float (&f)[8]) {
     f[2 * i + 1] = bf16_hi(w[i]);
   }
 }
-__device__ __forceinline__ float amax8(const float (&f)[8]) {
-  float m = 0.f;
+// max |x| as bits: magnitudes order as their bits, a NaN above all
+__device__ __forceinline__ uint32_t amax8(const float (&f)[8]) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
-  // fmaxf drops a NaN: keep it, so that the row's scale shows it
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = f[i] != f[i] ? f[i] : m;
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
   return m;
+}
+// f / sc of a row. The reciprocal's rounding (2^-23) is far below e4m3's half step (2^-4); scales
+// whose reciprocal leaves fp32's range are divided by.
+__device__ __forceinline__ void scale8(float (&f)[8], float sc) {
+  if (sc >= 7.52e-37f) {                      // 2^-120
+    const float r = 1.f / sc;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] /= sc;
+  }
 }
 
 template <bool FP8>
@@ -79,76 +89,91 @@ __global__ void __launch_bounds__(kApThreads) append_paged_kernel(const __grid_c
     s_cs[x] = make_float2(cs, sn);
   }
   __syncthreads();
-  for (int r = warp; r < count * p.Hkv; r += kApThreads / 32) {
-    const int t = r / p.Hkv, g = r - t * p.Hkv;
-    const long long pos = pos0 + t;
-    if (pos < 0 || pos >= most) continue;     // outside the table: not written
-    const int pg = static_cast<int>(pos / p.page_size);
-    const int ent = __ldg(p.table + static_cast<long long>(b) * p.max_pages + pg);
-    if (static_cast<unsigned>(ent) >= static_cast<unsigned>(p.num_pages)) continue;
-    const long long dst = (ent * p.page_stride + (pos - static_cast<long long>(pg) * p.page_size)) * p.Hkv + g;
-    const long long src = (static_cast<long long>(b) * p.n + i0 + t) * p.Hkv + g;
-    const bool is_k = lane < 24;
-    uint4 x0, x1 = make_uint4(0u, 0u, 0u, 0u);
-    if (is_k) {
-      x0 = *reinterpret_cast<const uint4*>(p.k + src * kDQK + lane * 8);
-    } else {
-      const uint4* pv = reinterpret_cast<const uint4*>(p.v + src * kDV + (lane - 24) * 16);
-      x0 = pv[0];
-      x1 = pv[1];
-    }
-    // the partner unit of the rotation, lane + nun or lane - nun
-    const int peer = lane < nun ? lane + nun : (lane < 2 * nun ? lane - nun : lane);
-    uint4 y;
-    y.x = __shfl_sync(0xffffffffu, x0.x, peer);
-    y.y = __shfl_sync(0xffffffffu, x0.y, peer);
-    y.z = __shfl_sync(0xffffffffu, x0.z, peer);
-    y.w = __shfl_sync(0xffffffffu, x0.w, peer);
-    float f[8], h[8];
-    unpack8(x0, f);
-    const bool turned = is_k && lane < 2 * nun;
-    if (turned) {
-      unpack8(y, h);
-      const float2* cs = s_cs + t * half + (lane < nun ? lane : lane - nun) * 8;
+  // two rows of the warp at a time, so that both rows' loads are in flight together
+  const int rows = count * p.Hkv;
+  const bool is_k = lane < 24;
+  const int peer = lane < nun ? lane + nun : (lane < 2 * nun ? lane - nun : lane);
+  for (int r0 = warp; r0 < rows; r0 += 2 * (kApThreads / 32)) {
+    uint32_t dst[2];
+    int tok[2];
+    bool put[2];
+    uint4 x0[2], x1[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 w = cs[i];
-        f[i] = lane < nun ? f[i] * w.x - h[i] * w.y : f[i] * w.x + h[i] * w.y;
+    for (int k = 0; k < 2; ++k) {
+      const int r = r0 + k * (kApThreads / 32);
+      put[k] = r < rows;
+      dst[k] = 0;
+      x0[k] = x1[k] = make_uint4(0u, 0u, 0u, 0u);
+      const int t = r / p.Hkv, g = r - t * p.Hkv;
+      tok[k] = put[k] ? t : 0;
+      const long long pos = pos0 + t;
+      put[k] = put[k] && pos >= 0 && pos < most;     // outside the table: not written
+      if (put[k]) {
+        const int pg = static_cast<int>(static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page_size));
+        const int ent = __ldg(p.table + static_cast<long long>(b) * p.max_pages + pg);
+        const long long src = (static_cast<long long>(b) * p.n + i0) * p.Hkv + r;
+        if (is_k) {
+          x0[k] = *reinterpret_cast<const uint4*>(p.k + src * kDQK + lane * 8);
+        } else {
+          const uint4* pv = reinterpret_cast<const uint4*>(p.v + src * kDV + (lane - 24) * 16);
+          x0[k] = pv[0];
+          x1[k] = pv[1];
+        }
+        put[k] = static_cast<unsigned>(ent) < static_cast<unsigned>(p.num_pages);
+        // (token, KV head) rows of a pool number less than 2^31 (checked by the host)
+        if (put[k]) dst[k] = static_cast<uint32_t>((ent * p.page_stride + static_cast<int>(pos) - pg * p.page_size) * p.Hkv + g);
       }
     }
-    if constexpr (FP8) {
-      unpack8(x1, h);                         // V: second unit
-      // |x| orders as its bits, a NaN above all
-      const uint32_t bf = __float_as_uint(amax8(f)) & 0x7fffffffu, bh = __float_as_uint(amax8(h)) & 0x7fffffffu;
-      const float ak = __uint_as_float(__reduce_max_sync(0xffffffffu, is_k ? bf : 0u));
-      const float av = __uint_as_float(__reduce_max_sync(0xffffffffu, is_k ? 0u : max(bf, bh)));
-      float sk = ak / 448.f, sv = av / 448.f;
-      sk = sk == 0.f ? 1.f : sk;
-      sv = sv == 0.f ? 1.f : sv;
-      const float sc = is_k ? sk : sv;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f[i] = f[i] / sc;
-        h[i] = h[i] / sc;
+    for (int k = 0; k < 2; ++k) {
+      // the partner unit of the rotation, lane + nun or lane - nun
+      uint4 y;
+      y.x = __shfl_sync(0xffffffffu, x0[k].x, peer);
+      y.y = __shfl_sync(0xffffffffu, x0[k].y, peer);
+      y.z = __shfl_sync(0xffffffffu, x0[k].z, peer);
+      y.w = __shfl_sync(0xffffffffu, x0[k].w, peer);
+      if (!put[k]) continue;                         // the same for the whole warp
+      float f[8], h[8];
+      unpack8(x0[k], f);
+      if (lane < 2 * nun) {
+        unpack8(y, h);
+        const float2* cs = s_cs + tok[k] * half + (lane < nun ? lane : lane - nun) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 w = cs[i];
+          f[i] = lane < nun ? f[i] * w.x - h[i] * w.y : f[i] * w.x + h[i] * w.y;
+        }
       }
-      const uint2 lo = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
-      if (is_k) {
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kc) + dst * kDQK + lane * 8) = lo;
+      const uint64_t d = dst[k];
+      if constexpr (FP8) {
+        unpack8(x1[k], h);                           // V: second unit (zeros on K lanes)
+        const uint32_t top = max(amax8(f), amax8(h));
+        float sk = __uint_as_float(__reduce_max_sync(0xffffffffu, is_k ? top : 0u)) / 448.f;
+        float sv = __uint_as_float(__reduce_max_sync(0xffffffffu, is_k ? 0u : top)) / 448.f;
+        sk = sk == 0.f ? 1.f : sk;
+        sv = sv == 0.f ? 1.f : sv;
+        const float sc = is_k ? sk : sv;
+        scale8(f, sc);
+        const uint2 lo = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+        if (is_k) {
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kc) + d * kDQK + lane * 8) = lo;
+        } else {
+          scale8(h, sc);
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.vc) + d * kDV + (lane - 24) * 16) =
+              make_uint4(lo.x, lo.y, e4m3x4(h[0], h[1], h[2], h[3]), e4m3x4(h[4], h[5], h[6], h[7]));
+        }
+        if (lane == 0) p.ks[d] = sk;
+        if (lane == 24) p.vs[d] = sv;
       } else {
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.vc) + dst * kDV + (lane - 24) * 16) =
-            make_uint4(lo.x, lo.y, e4m3x4(h[0], h[1], h[2], h[3]), e4m3x4(h[4], h[5], h[6], h[7]));
-      }
-      if (lane == 0) p.ks[dst] = sk;
-      if (lane == 24) p.vs[dst] = sv;
-    } else {
-      if (is_k) {
-        if (turned)
-          x0 = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.kc) + dst * kDQK + lane * 8) = x0;
-      } else {
-        uint4* pv = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.vc) + dst * kDV + (lane - 24) * 16);
-        pv[0] = x0;
-        pv[1] = x1;
+        if (is_k) {
+          if (lane < 2 * nun)
+            x0[k] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.kc) + d * kDQK + lane * 8) = x0[k];
+        } else {
+          uint4* pv = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.vc) + d * kDV + (lane - 24) * 16);
+          pv[0] = x0[k];
+          pv[1] = x1[k];
+        }
       }
     }
   }

@@ -19,10 +19,13 @@
 //
 // Tile. Rows arrive by 16-byte cp.async, kPgStages tiles in flight, without a pause where one
 // unit ends and the next begins. Four warps share one softmax: warp w scores KT/4 of the keys
-// (S = Q K^T, m16n8k16 with the group's heads as rows), the tile's row maxima meet in shared
-// memory, the weights P are written there, and warp w multiplies all of P with its 32 columns
-// of V. So a warp holds 16 x 32 of O (16 registers a thread) instead of 16 x 128, and no state
-// is merged across warps at a unit's end but the row sums.
+// (S = Q K^T, m16n8k16 with the group's heads as rows), the weights P go to shared memory, and
+// warp w multiplies all of P with its 32 columns of V. So a warp holds 16 x 32 of O (16 registers
+// a thread) instead of 16 x 128, and no state is merged across warps at a unit's end but the row
+// sums. The row references move only when a score lies 2^8 above them (and at a unit's first
+// tile): a thread checks its own scores, P is written on trust, and the barrier that publishes P
+// also says whether some thread disagrees, in which case the maxima meet in shared memory and P
+// is written again. So a tile costs two barriers and no exchange of maxima.
 // Precision: bf16 products are exact with fp32 sums. P is carried as two bf16 terms (high part
 // and remainder, 16 significant bits), so that the only visible rounding is that of the output:
 // one bf16 term made the output's error 1.4 times that of the rounding alone. FP8 pages: bytes
@@ -50,7 +53,7 @@ struct PagedParams {
   int4* hdr;                  // [min(B * Hkv, nctas)]: (unit, first CTA, last CTA, -) of a cut unit
   float* part_ml;             // [2 nctas, G, 2]  (m in log2 units, l)
   float* part_o;              // [2 nctas, G, 128]
-  long long page_stride;      // tokens between pages
+  int page_stride;            // tokens between pages
   int B, Hq, Hkv, page_size, max_pages, num_pages, window, n_first, nctas;
   uint32_t div_mul;           // t / page_size = (t * div_mul) >> div_shift for t < 2^31
   int div_shift;
@@ -70,7 +73,7 @@ struct PagedCfg {
   static constexpr int ROWS = KT / (kPgThreads / TPR);      // rows per thread (2)
   static constexpr int OFF_V = KT * KROW;
   static constexpr int OFF_Q = OFF_V + KT * VROW;           // a unit's 16 query rows (its first tile only)
-  static constexpr int OFF_OK = OFF_Q + 16 * kKRow;         // int [KT]: the key names a cached token
+  static constexpr int OFF_OK = OFF_Q + 16 * kKRow;         // float [KT]: 0, or -inf: no cached token
   static constexpr int OFF_SC = OFF_OK + KT * 4;            // float [2][KT] K and V scales
   static constexpr int STAGE = OFF_SC + (FP8 ? KT * 8 : 0);
   static constexpr int PROW = KT * 2 + 16;                  // bytes per row of P (padded: no bank conflicts)
@@ -98,6 +101,15 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
   s.nf = s.lo < p.n_first ? s.lo : p.n_first;
   s.nkeys = s.nf + L - s.lo;
   return s;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t f16_bits(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 template <int KT>
 __device__ __forceinline__ int paged_tiles(int nkeys) {   // an empty unit keeps one (masked) tile
@@ -171,6 +183,8 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
   const int b0 = lb, g0 = lg, j0 = lj, t0 = lt;
   const int* tab = p.table + static_cast<long long>(lb) * p.max_pages;
   const int lrow = tid / C::TPR, lu = tid % C::TPR;
+  const uint8_t* kbase = static_cast<const uint8_t*>(p.k) + lu * 16;
+  const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + lu * 16;
   int ent[2], off[2];
   bool unit_start = true;                     // the next tile to issue needs its unit's Q
   auto fetch = [&]() {                        // page entries of the iterator's tile
@@ -194,9 +208,10 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
       const int row = i * (KT / 2) + lrow;
       const bool ok = static_cast<unsigned>(ent[i]) < static_cast<unsigned>(p.num_pages);
       const uint32_t sz = ok ? 16u : 0u;
-      const long long r = (ok ? ent[i] * p.page_stride + off[i] : 0) * p.Hkv + lg;
-      const uint8_t* kg = static_cast<const uint8_t*>(p.k) + r * C::KROW + lu * 16;
-      const uint8_t* vg = static_cast<const uint8_t*>(p.v) + r * C::VROW + lu * 16;
+      // (token, KV head) rows of a pool number less than 2^31 (checked by the host)
+      const uint32_t r = static_cast<uint32_t>((ok ? ent[i] * p.page_stride + off[i] : 0) * p.Hkv + lg);
+      const uint8_t* kg = kbase + static_cast<uint64_t>(r) * C::KROW;
+      const uint8_t* vg = vbase + static_cast<uint64_t>(r) * C::VROW;
       if constexpr (FP8) {
         // K rows as they are (192 bytes: eight rows' 16-byte units cover the banks evenly); V
         // rows swizzled for the transposed ldmatrix
@@ -213,7 +228,7 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
 #pragma unroll
         for (int pp = 0; pp < 2; ++pp) cp_async16(st + C::OFF_V + row * C::VROW + pp * 128 + sw, vg + pp * 128, sz);
       }
-      if (lu == 0) *reinterpret_cast<int*>(smem + stage * C::STAGE + C::OFF_OK + row * 4) = ok;
+      if (lu == 0) *reinterpret_cast<float*>(smem + stage * C::STAGE + C::OFF_OK + row * 4) = ok ? 0.f : -INFINITY;
     }
     if (unit_start) {                         // 16 rows of Q (zero above the group), swizzled
       const uint8_t* qg = reinterpret_cast<const uint8_t*>(p.q + (static_cast<long long>(lb) * p.Hq + lg * G) * kDQK);
@@ -237,7 +252,7 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
       }
     }
   };
-  const long long ntiles = e - a;
+  const int ntiles = static_cast<int>(e - a);   // (the host keeps runs below 2^31 tiles)
   fetch();
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s) {
@@ -262,7 +277,7 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
   float* s_l = reinterpret_cast<float*>(smem + C::OFF_L);
   const int mi = lane >> 3, r8 = lane & 7;
   int stage = 0;
-  for (long long it = 0; it < ntiles; ++it) {
+  for (int it = 0; it < ntiles; ++it) {
     cp_async_wait<NS - 2>();
     __syncthreads();                          // the tile has landed; the previous one is consumed
     {
@@ -278,6 +293,7 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
     }
     const uint32_t sK = s_base + stage * C::STAGE, sV = sK + C::OFF_V, sQ = sK + C::OFF_Q;
     const uint8_t* st_ptr = smem + stage * C::STAGE;
+    bool need = fresh;                        // the references have to move
     if (fresh) {
       fresh = false;
       if constexpr (FP8) {
@@ -345,99 +361,121 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
       for (int x = 0; x < 4; ++x) s[0][x] = acc[0][x] + acc[1][x];
     }
 
-    // masked keys to -inf (log2 domain), row maxima of the warp's keys
-    const int* ok = reinterpret_cast<const int*>(st_ptr + C::OFF_OK);
+    // scores in the log2 domain, masked keys at -inf; does any lie above its reference?
+    const float* msk = reinterpret_cast<const float*>(st_ptr + C::OFF_OK);
     const float* ksc = reinterpret_cast<const float*>(st_ptr + C::OFF_SC);
-    float lg[NT][2], vsg[NT][2];              // log2 |v scale| and the scale (FP8)
-    float mx0 = -INFINITY, mx1 = -INFINITY, rx0 = -INFINITY, rx1 = -INFINITY;
+    float lgv[NT][2], vsg[NT][2];             // (FP8) log2 |v scale|, and the scale
+    const float lim0 = m0 + 8.f, lim1 = m1 + 8.f, rlim0 = R0 + 8.f, rlim1 = R1 + 8.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int key = warp * (KT / 4) + nt * 8 + tq * 2 + x;
-        const bool valid = ok[key] != 0;
-        float f = p.scale_log2;
-        if constexpr (FP8) {
-          f *= ksc[key];
-          vsg[nt][x] = ksc[KT + key];
-          lg[nt][x] = log2f(fabsf(vsg[nt][x]));
-        }
-        s[nt][x] = valid ? s[nt][x] * f : -INFINITY;
-        s[nt][2 + x] = valid ? s[nt][2 + x] * f : -INFINITY;
-        mx0 = fmaxf(mx0, s[nt][x]);
-        mx1 = fmaxf(mx1, s[nt][2 + x]);
-        if constexpr (FP8) {
-          rx0 = fmaxf(rx0, s[nt][x] + lg[nt][x]);
-          rx1 = fmaxf(rx1, s[nt][2 + x] + lg[nt][x]);
-        }
-      }
-    }
-#pragma unroll
-    for (int sh = 1; sh < 4; sh <<= 1) {
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
+      const int key = warp * (KT / 4) + nt * 8 + tq * 2;
+      const float2 mk = *reinterpret_cast<const float2*>(msk + key);
+      float f0 = p.scale_log2, f1 = p.scale_log2;
       if constexpr (FP8) {
-        rx0 = fmaxf(rx0, __shfl_xor_sync(0xffffffffu, rx0, sh));
-        rx1 = fmaxf(rx1, __shfl_xor_sync(0xffffffffu, rx1, sh));
+        const float2 kk = *reinterpret_cast<const float2*>(ksc + key);
+        const float2 vv = *reinterpret_cast<const float2*>(ksc + KT + key);
+        f0 *= kk.x;
+        f1 *= kk.y;
+        vsg[nt][0] = vv.x;
+        vsg[nt][1] = vv.y;
+        lgv[nt][0] = lg2(fabsf(vv.x));
+        lgv[nt][1] = lg2(fabsf(vv.y));
       }
+      s[nt][0] = fmaf(s[nt][0], f0, mk.x);
+      s[nt][1] = fmaf(s[nt][1], f1, mk.y);
+      s[nt][2] = fmaf(s[nt][2], f0, mk.x);
+      s[nt][3] = fmaf(s[nt][3], f1, mk.y);
+      need |= s[nt][0] > lim0 || s[nt][1] > lim0 || s[nt][2] > lim1 || s[nt][3] > lim1;
+      if constexpr (FP8)
+        need |= s[nt][0] + lgv[nt][0] > rlim0 || s[nt][1] + lgv[nt][1] > rlim0 || s[nt][2] + lgv[nt][0] > rlim1 ||
+                s[nt][3] + lgv[nt][1] > rlim1;
     }
-    if (tq == 0) {
-      s_mx[gq * 4 + warp] = mx0;
-      s_mx[(gq + 8) * 4 + warp] = mx1;
-      if constexpr (FP8) {
-        s_mx[64 + gq * 4 + warp] = rx0;
-        s_mx[64 + (gq + 8) * 4 + warp] = rx1;
+    float d0, d1;                             // this tile's share of the row sums
+    auto write_p = [&]() {
+      const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
+      const float rr0 = R0 == -INFINITY ? 0.f : R0, rr1 = R1 == -INFINITY ? 0.f : R1;
+      d0 = d1 = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float p0 = ex2(s[nt][0] - ref0), p1 = ex2(s[nt][1] - ref0);
+        const float p2 = ex2(s[nt][2] - ref1), p3 = ex2(s[nt][3] - ref1);
+        d0 += p0 + p1;
+        d1 += p2 + p3;
+        const uint32_t col = static_cast<uint32_t>(warp * (KT / 4) + nt * 8 + tq * 2) * 2;
+        uint32_t* w0 = reinterpret_cast<uint32_t*>(smem + C::OFF_P + gq * C::PROW + col);
+        uint32_t* w1 = reinterpret_cast<uint32_t*>(smem + C::OFF_P + (gq + 8) * C::PROW + col);
+        if constexpr (FP8) {
+          *w0 = f16_bits(copysignf(ex2(s[nt][0] + lgv[nt][0] - rr0), vsg[nt][0]),
+                         copysignf(ex2(s[nt][1] + lgv[nt][1] - rr0), vsg[nt][1]));
+          *w1 = f16_bits(copysignf(ex2(s[nt][2] + lgv[nt][0] - rr1), vsg[nt][0]),
+                         copysignf(ex2(s[nt][3] + lgv[nt][1] - rr1), vsg[nt][1]));
+        } else {
+          const uint32_t h0 = pack_bf16(p0, p1), h1 = pack_bf16(p2, p3);
+          *w0 = h0;
+          *w1 = h1;
+          w0[16 * C::PROW / 4] = pack_bf16(p0 - bf16_lo(h0), p1 - bf16_hi(h0));
+          w1[16 * C::PROW / 4] = pack_bf16(p2 - bf16_lo(h1), p3 - bf16_hi(h1));
+        }
       }
-    }
-    __syncthreads();
-    // the tile's row maxima move the running references
-    auto move = [&](float& m, const float* at) -> float {
-      const float4 x = *reinterpret_cast<const float4*>(at);
-      const float mn = fmaxf(fmaxf(m, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
-      const float al = ex2(m - (mn == -INFINITY ? 0.f : mn));   // 0 from -inf
-      m = mn;
-      return al;
     };
-    const float al0 = move(m0, s_mx + gq * 4), al1 = move(m1, s_mx + (gq + 8) * 4);
-    float ao0 = al0, ao1 = al1;
-    if constexpr (FP8) {
-      ao0 = move(R0, s_mx + 64 + gq * 4);
-      ao1 = move(R1, s_mx + 64 + (gq + 8) * 4);
-    }
-    const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
-    const float rr0 = R0 == -INFINITY ? 0.f : R0, rr1 = R1 == -INFINITY ? 0.f : R1;
-    l0 *= al0;
-    l1 *= al1;
+    write_p();
+    if (__syncthreads_or(need)) {
+      // the tile's row maxima move the references; O and the sums follow; P again
+      float mx0 = -INFINITY, mx1 = -INFINITY, rx0 = -INFINITY, rx1 = -INFINITY;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float p0 = ex2(s[nt][0] - ref0), p1 = ex2(s[nt][1] - ref0);
-      const float p2 = ex2(s[nt][2] - ref1), p3 = ex2(s[nt][3] - ref1);
-      l0 += p0 + p1;
-      l1 += p2 + p3;
-      const uint32_t col = static_cast<uint32_t>(warp * (KT / 4) + nt * 8 + tq * 2) * 2;
-      uint32_t* w0 = reinterpret_cast<uint32_t*>(smem + C::OFF_P + gq * C::PROW + col);
-      uint32_t* w1 = reinterpret_cast<uint32_t*>(smem + C::OFF_P + (gq + 8) * C::PROW + col);
-      if constexpr (FP8) {
-        *w0 = pack_f16(copysignf(ex2(s[nt][0] + lg[nt][0] - rr0), vsg[nt][0]),
-                       copysignf(ex2(s[nt][1] + lg[nt][1] - rr0), vsg[nt][1]));
-        *w1 = pack_f16(copysignf(ex2(s[nt][2] + lg[nt][0] - rr1), vsg[nt][0]),
-                       copysignf(ex2(s[nt][3] + lg[nt][1] - rr1), vsg[nt][1]));
-      } else {
-        const uint32_t h0 = pack_bf16(p0, p1), h1 = pack_bf16(p2, p3);
-        *w0 = h0;
-        *w1 = h1;
-        w0[16 * C::PROW / 4] = pack_bf16(p0 - bf16_lo(h0), p1 - bf16_hi(h0));
-        w1[16 * C::PROW / 4] = pack_bf16(p2 - bf16_lo(h1), p3 - bf16_hi(h1));
+      for (int nt = 0; nt < NT; ++nt) {
+        mx0 = fmaxf(mx0, fmaxf(s[nt][0], s[nt][1]));
+        mx1 = fmaxf(mx1, fmaxf(s[nt][2], s[nt][3]));
+        if constexpr (FP8) {
+          rx0 = fmaxf(rx0, fmaxf(s[nt][0] + lgv[nt][0], s[nt][1] + lgv[nt][1]));
+          rx1 = fmaxf(rx1, fmaxf(s[nt][2] + lgv[nt][0], s[nt][3] + lgv[nt][1]));
+        }
       }
-    }
-    __syncthreads();
-
-    // O (this warp's 32 columns) = O alpha + P V
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      o[nt][0] *= ao0; o[nt][1] *= ao0;
-      o[nt][2] *= ao1; o[nt][3] *= ao1;
+      for (int sh = 1; sh < 4; sh <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
+        if constexpr (FP8) {
+          rx0 = fmaxf(rx0, __shfl_xor_sync(0xffffffffu, rx0, sh));
+          rx1 = fmaxf(rx1, __shfl_xor_sync(0xffffffffu, rx1, sh));
+        }
+      }
+      if (tq == 0) {
+        s_mx[gq * 4 + warp] = mx0;
+        s_mx[(gq + 8) * 4 + warp] = mx1;
+        if constexpr (FP8) {
+          s_mx[64 + gq * 4 + warp] = rx0;
+          s_mx[64 + (gq + 8) * 4 + warp] = rx1;
+        }
+      }
+      __syncthreads();
+      auto move = [&](float& m, const float* at) -> float {
+        const float4 x = *reinterpret_cast<const float4*>(at);
+        const float mn = fmaxf(fmaxf(m, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
+        const float al = ex2(m - (mn == -INFINITY ? 0.f : mn));   // 0 from -inf
+        m = mn;
+        return al;
+      };
+      const float al0 = move(m0, s_mx + gq * 4), al1 = move(m1, s_mx + (gq + 8) * 4);
+      float ao0 = al0, ao1 = al1;
+      if constexpr (FP8) {
+        ao0 = move(R0, s_mx + 64 + gq * 4);
+        ao1 = move(R1, s_mx + 64 + (gq + 8) * 4);
+      }
+      l0 *= al0;
+      l1 *= al1;
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        o[nt][0] *= ao0; o[nt][1] *= ao0;
+        o[nt][2] *= ao1; o[nt][3] *= ao1;
+      }
+      write_p();
+      __syncthreads();
     }
+    l0 += d0;
+    l1 += d1;
+
+    // O (this warp's 32 columns) += P V
 #pragma unroll
     for (int ks = 0; ks < KT / 16; ++ks) {
       const uint32_t prow = s_base + C::OFF_P + (((mi & 1) << 3) + r8) * C::PROW + ks * 32 + (mi >> 1) * 16;
@@ -574,54 +612,71 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
 
 // Joins the slots of one cut unit (blockIdx.x) for one query head of its group (blockIdx.y):
 // M = max(sink, max m_c), o = sum o_c 2^(m_c - M) / (2^(sink - M) + sum l_c 2^(m_c - M)). Warp w
-// takes slots w, w + 4, ..., eight rows of 512 bytes in flight.
+// takes slots w, w + 4, ..., eight of them (state and row together) in flight, under a running
+// maximum of its own: two trips to memory, the header's and the slots'.
 __global__ void __launch_bounds__(128) decode_paged_combine_kernel(const PagedParams p) {
   __shared__ float4 s_o[4][32];
-  __shared__ float s_l[4];
+  __shared__ float2 s_ml[4];
   pdl_wait();
   pdl_trigger();
   const int4 h = p.hdr[blockIdx.x];
   if (h.y < 0) return;
   const int G = gridDim.y, r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int np = h.z - h.y + 1;
-  const int b = h.x / p.Hkv, g = h.x - b * p.Hkv;
-  auto slot_of = [&](int i) -> long long { return (2LL * (h.y + i) + (i == 0 ? 1 : 0)) * G + r; };
-  float M = -INFINITY;
-  for (int i = threadIdx.x & 31; i < np; i += 32) M = fmaxf(M, p.part_ml[slot_of(i) * 2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const int head = g * G + r;
-  const float sk = p.sink ? p.sink[head] * 1.4426950408889634f : -INFINITY;
-  M = fmaxf(M, sk);
-  const float ref = M == -INFINITY ? 0.f : M;
+  float M = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 8
-  for (int i = warp; i < np; i += 4) {
-    const long long s = slot_of(i);
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + s * 2);
-    const float4 x = *reinterpret_cast<const float4*>(p.part_o + s * kDV + lane * 4);
-    const float w = ex2(ml.x - ref);
-    l += ml.y * w;
-    acc.x += x.x * w;
-    acc.y += x.y * w;
-    acc.z += x.z * w;
-    acc.w += x.w * w;
+  for (int i0 = warp; i0 < np; i0 += 32) {
+    float2 ml[8];
+    float4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + 4 * k;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < np) {
+        const long long s = (2LL * (h.y + i) + (i == 0 ? 1 : 0)) * G + r;
+        ml[k] = *reinterpret_cast<const float2*>(p.part_ml + s * 2);
+        x[k] = *reinterpret_cast<const float4*>(p.part_o + s * kDV + lane * 4);
+      }
+    }
+    float mn = M;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mn = fmaxf(mn, ml[k].x);
+    const float ref = mn == -INFINITY ? 0.f : mn, al = ex2(M - ref);
+    M = mn;
+    l *= al;
+    acc.x *= al; acc.y *= al; acc.z *= al; acc.w *= al;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float w = ex2(ml[k].x - ref);
+      l += ml[k].y * w;
+      acc.x += x[k].x * w;
+      acc.y += x[k].y * w;
+      acc.z += x[k].z * w;
+      acc.w += x[k].w * w;
+    }
   }
   s_o[warp][lane] = acc;
-  if (lane == 0) s_l[warp] = l;
+  if (lane == 0) s_ml[warp] = make_float2(M, l);
   __syncthreads();
   if (warp != 0) return;
+  const int b = h.x / p.Hkv, head = (h.x - b * p.Hkv) * G + r;
+  const float sk = p.sink ? p.sink[head] * 1.4426950408889634f : -INFINITY;
+  float m = sk;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) m = fmaxf(m, s_ml[w].x);
+  const float ref = m == -INFINITY ? 0.f : m;
   float Lt = p.sink ? ex2(sk - ref) : 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int w = 0; w < 4; ++w) Lt += s_l[w];
-#pragma unroll
-  for (int w = 1; w < 4; ++w) {
+  for (int w = 0; w < 4; ++w) {
+    const float f = ex2(s_ml[w].x - ref);
     const float4 x = s_o[w][lane];
-    acc.x += x.x;
-    acc.y += x.y;
-    acc.z += x.z;
-    acc.w += x.w;
+    Lt += s_ml[w].y * f;
+    acc.x += x.x * f;
+    acc.y += x.y * f;
+    acc.z += x.z * f;
+    acc.w += x.w * f;
   }
   const float f = Lt == 0.f ? 0.f : 1.f / Lt;
   const long long bh = static_cast<long long>(b) * p.Hq + head;

@@ -756,11 +756,13 @@ mimo_status run_prefill_chunk(const mimo_shape* s, const void* q, const void* k,
 }
 
 // ---------------------------------------------------------------- paged KV cache
-mimo_status check_pages(const mimo_pages* pg) {
+mimo_status check_pages(const mimo_pages* pg, int hkv) {
   if (!pg) return MIMO_ERR_NULL;
   if (pg->max_pages < 1 || pg->num_pages < 1 || pg->page_size < 1 || pg->page_stride_tokens < pg->page_size)
     return MIMO_ERR_SHAPE;
   if (static_cast<long long>(pg->max_pages) * pg->page_size > 0x7fffffffLL) return MIMO_ERR_UNSUPPORTED;
+  // (token, KV head) rows of a pool are counted in 32 bits
+  if (pg->page_stride_tokens > 0x7fffffffLL / pg->num_pages / hkv) return MIMO_ERR_UNSUPPORTED;
   return MIMO_OK;
 }
 
@@ -781,7 +783,7 @@ PagedPlan plan_paged(const mimo_shape* s, const mimo_pages* pg, int window, int 
   if (window > 0) keys = std::min(keys, static_cast<long long>(window) + n_first);
   pl.split = keys > tile;
   const long long tiles = (keys + tile - 1) / tile;
-  pl.nctas = static_cast<int>(std::min<long long>(2LL * sms, U > 2LL * sms ? U : U * tiles));
+  pl.nctas = static_cast<int>(std::min<long long>(2LL * sms, U * tiles));
   if (!pl.split) return pl;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = 2 * static_cast<size_t>(pl.nctas) * G;
@@ -814,10 +816,14 @@ mimo_status run_paged(const mimo_shape* s, const void* q, const void* k, const v
   mimo_status e = check_heads(s);
   if (e != MIMO_OK) return e;
   if (!q || !k || !v || !lengths || !out || !pg || !pg->block_table || (FP8 && (!ks || !vs))) return MIMO_ERR_NULL;
-  e = check_pages(pg);
+  e = check_pages(pg, s->n_kv_heads);
   if (e != MIMO_OK) return e;
   if (n_first < 0) return MIMO_ERR_SHAPE;
   if (static_cast<long long>(s->batch) * s->n_kv_heads > 0x7fffffffLL) return MIMO_ERR_UNSUPPORTED;
+  // tiles of a run are counted in 32 bits
+  if (static_cast<long long>(s->batch) * s->n_kv_heads >
+      (64LL << 31) / ((static_cast<long long>(pg->max_pages) * pg->page_size + 31) / 32))
+    return MIMO_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lengths, 4) ||
       !aligned(pg->block_table, 4) || (sink && !aligned(sink, 4)) || (lse && !aligned(lse, 4)) ||
       (FP8 && (!aligned(ks, 4) || !aligned(vs, 4))))
@@ -843,7 +849,7 @@ mimo_status run_paged(const mimo_shape* s, const void* q, const void* k, const v
     prm.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.off_ml);
     prm.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.off_o);
   }
-  prm.page_stride = pg->page_stride_tokens;
+  prm.page_stride = static_cast<int>(pg->page_stride_tokens);
   prm.B = s->batch;
   prm.Hq = s->n_q_heads;
   prm.Hkv = s->n_kv_heads;
@@ -860,8 +866,10 @@ mimo_status run_paged(const mimo_shape* s, const void* q, const void* k, const v
   prm.div_shift = 31 + l;
   prm.div_mul = static_cast<uint32_t>(((1ULL << (31 + l)) + pg->page_size - 1) / pg->page_size);
   prm.scale_log2 = scale_log2_of(s);
+#ifdef MIMO_DEBUG   // the only reports of these kernels are the debug builds' (no wait can give up)
   prm.err = device_error_ptr(dev);
   if (!prm.err) return MIMO_ERR_CUDA;
+#endif
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (s->n_q_heads / s->n_kv_heads) {
     case 1: return launch_paged<1, FP8>(prm, pl.split, st);
@@ -880,7 +888,7 @@ mimo_status run_append_paged(const mimo_shape* s, const void* k_new, const void*
   if (e != MIMO_OK) return e;
   if (!k_new || !v_new || !positions || !kc || !vc || !pg || !pg->block_table || (FP8 && (!ks || !vs)))
     return MIMO_ERR_NULL;
-  e = check_pages(pg);
+  e = check_pages(pg, s->n_kv_heads);
   if (e != MIMO_OK) return e;
   if (s->seqlen < 1) return MIMO_ERR_SHAPE;
   if (rot < 0 || rot > mimo::kDQK) return MIMO_ERR_SHAPE;
@@ -905,7 +913,7 @@ mimo_status run_append_paged(const mimo_shape* s, const void* k_new, const void*
   prm.table = pg->block_table;
   prm.pos = positions;
   prm.n_new = n_new;
-  prm.page_stride = pg->page_stride_tokens;
+  prm.page_stride = static_cast<int>(pg->page_stride_tokens);
   prm.B = s->batch;
   prm.n = s->seqlen;
   prm.Hkv = s->n_kv_heads;
@@ -920,14 +928,14 @@ mimo_status run_append_paged(const mimo_shape* s, const void* k_new, const void*
 }
 
 // ---------------------------------------------------------------- draft verification
-template <typename E>
+template <typename E, bool VEC>
 mimo_status launch_verify(mimo::VerifyParams prm, int B, cudaStream_t st) {
-  // a cluster of up to 8 CTAs shares a row; a short row takes fewer, so that a warp's piece
-  // keeps at least 64 tokens
+  // a cluster of up to 8 CTAs shares a row; a short row takes fewer, so that the pieces of 256
+  // values and more fill the warps
   int c = 1;
-  while (c < mimo::kVfMaxCluster && static_cast<long long>(c) * mimo::kVfWarps * 128 <= prm.V) c *= 2;
+  while (c < mimo::kVfMaxCluster && static_cast<long long>(c) * mimo::kVfWarps * 256 < prm.V) c *= 2;
   const int pieces = c * mimo::kVfWarps;
-  prm.piece = static_cast<int>(((static_cast<long long>(prm.V) + pieces - 1) / pieces + 31) / 32 * 32);
+  prm.piece = static_cast<int>(((static_cast<long long>(prm.V) + pieces - 1) / pieces + 255) / 256 * 256);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(c), static_cast<unsigned>(B));
   cfg.blockDim = dim3(mimo::kVfThreads);
@@ -939,7 +947,7 @@ mimo_status launch_verify(mimo::VerifyParams prm, int B, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, mimo::verify_kernel<E>, static_cast<const mimo::VerifyParams>(prm)) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, mimo::verify_kernel<E, VEC>, static_cast<const mimo::VerifyParams>(prm)) != cudaSuccess) {
     cudaGetLastError();
     return MIMO_ERR_CUDA;
   }
@@ -1221,7 +1229,7 @@ mimo_status mimo_attn_decode_mq(const mimo_shape* s, const void* q, const void* 
 }
 
 size_t mimo_attn_decode_paged_workspace_size(const mimo_shape* s, const mimo_pages* pages, int window, int n_first) {
-  if (check_heads(s) != MIMO_OK || check_pages(pages) != MIMO_OK || n_first < 0) return 0;
+  if (check_heads(s) != MIMO_OK || check_pages(pages, s->n_kv_heads) != MIMO_OK || n_first < 0) return 0;
   if (static_cast<long long>(s->batch) * s->n_kv_heads > 0x7fffffffLL) return 0;
   const int sms = sm_count_for(current_device());   // one size serves the bf16 and the FP8 call
   return std::max(plan_paged(s, pages, window, n_first, false, sms).bytes,
@@ -1283,8 +1291,12 @@ mimo_status mimo_attn_verify_drafts(int batch, int n_drafts, int vocab, int prob
   prm.T = n_drafts;
   prm.V = vocab;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return probs_type == MIMO_PROBS_F32 ? launch_verify<float>(prm, batch, st)
-                                      : launch_verify<__nv_bfloat16>(prm, batch, st);
+  // 16-byte loads where every row starts on 16 bytes
+  const int per16 = probs_type == MIMO_PROBS_F32 ? 4 : 8;
+  const bool vec = vocab % per16 == 0 && aligned(prm.p, 16) && aligned(prm.q, 16);
+  if (probs_type == MIMO_PROBS_F32)
+    return vec ? launch_verify<float, true>(prm, batch, st) : launch_verify<float, false>(prm, batch, st);
+  return vec ? launch_verify<__nv_bfloat16, true>(prm, batch, st) : launch_verify<__nv_bfloat16, false>(prm, batch, st);
 }
 
 size_t mimo_attn_decode_mq_workspace_size(const mimo_shape* s, int cache_kind, int cache_capacity,

@@ -36,7 +36,7 @@ struct VerifyParams {
   int* accepted;              // [B]
   int* tokens;                // [B, T + 1]
   int T, V;
-  int piece;                  // elements per warp of the cluster
+  int piece;                  // elements per warp of the cluster (a multiple of 256)
 };
 
 __device__ __forceinline__ float vf_load(const float* x) { return __ldg(x); }
@@ -64,7 +64,77 @@ __device__ __forceinline__ double vf_warp_scan(double x) {   // inclusive
   return x;
 }
 
+// W consecutive values of a row as floats, one 16-byte load (rows start on 16 bytes).
 template <typename E>
+struct VfVec;
+template <>
+struct VfVec<float> {
+  static constexpr int W = 4, U = 4;          // values per load, loads of a row in flight
+  static __device__ __forceinline__ void get(const uint4& x, float (&f)[W]) {
+    f[0] = __uint_as_float(x.x); f[1] = __uint_as_float(x.y); f[2] = __uint_as_float(x.z); f[3] = __uint_as_float(x.w);
+  }
+};
+template <>
+struct VfVec<__nv_bfloat16> {
+  static constexpr int W = 8, U = 2;
+  static __device__ __forceinline__ void get(const uint4& x, float (&f)[W]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(w[i]);
+      f[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+};
+
+// Sum of the weights of [v0, v1) by one warp (each lane returns its share). VEC: 16-byte loads,
+// which need rows that start on 16 bytes (V a multiple of W); otherwise one value per lane and
+// load, eight loads in flight.
+template <typename E, bool VEC>
+__device__ __forceinline__ double vf_piece(const E* p, const E* q, int hot, int v0, int v1) {
+  using X = VfVec<E>;
+  const int lane = threadIdx.x & 31;
+  double sum = 0.0;
+  if constexpr (VEC) {
+    constexpr int W = X::W, U = X::U;
+    for (int v = v0 + lane * W; v < v1; v += 32 * W * U) {
+      uint4 a[U], b[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = v + u * 32 * W;
+        a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (at < v1) {
+          a[u] = __ldg(reinterpret_cast<const uint4*>(p + at));
+          if (q) b[u] = __ldg(reinterpret_cast<const uint4*>(q + at));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float x[W], y[W];
+        X::get(a[u], x);
+        X::get(b[u], y);
+#pragma unroll
+        for (int e = 0; e < W; ++e) sum += vf_weight(x[e], v + u * 32 * W + e == hot ? 1.f : y[e]);
+      }
+    }
+  } else {
+    constexpr int U = 8;
+    for (int v = v0 + lane; v < v1; v += 32 * U) {
+      float x[U], y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = v + u * 32;
+        x[u] = at < v1 ? vf_load(p + at) : 0.f;
+        y[u] = at < v1 && q ? vf_load(q + at) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) sum += vf_weight(x[u], v + u * 32 == hot ? 1.f : y[u]);
+    }
+  }
+  return sum;
+}
+
+template <typename E, bool VEC>
 __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams prm) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
@@ -107,33 +177,28 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
   const int a = s_acc;
   const E* p = p0 + static_cast<long long>(a) * V;
   bool minus = a < n;                         // subtract the draft's row
-  const E* q = prm.q ? q0 + static_cast<long long>(a < T ? a : 0) * V : nullptr;
-  const int hot = minus && !prm.q ? __ldg(draft + a) : -1;
-  auto weight = [&](int v) -> double {
-    const float pv = vf_load(p + v);
-    float qv = 0.f;
-    if (minus) qv = q ? vf_load(q + v) : (v == hot ? 1.f : 0.f);
-    return vf_weight(pv, qv);
-  };
-
+  const E* q = prm.q && minus ? q0 + static_cast<long long>(a) * V : nullptr;
+  int hot = minus && !prm.q ? __ldg(draft + a) : -1;
   const int pieces = C * kVfWarps, mine = rank * kVfWarps + warp;
+  const int per = (pieces + 31) / 32;         // pieces a lane scans (at most 4)
   for (;;) {
     const long long v0 = static_cast<long long>(mine) * prm.piece;
-    const long long v1 = min(v0 + prm.piece, static_cast<long long>(V));
     double sum = 0.0;
-#pragma unroll 8
-    for (long long v = v0 + lane; v < v1; v += 32) sum += weight(static_cast<int>(v));
+    if (v0 < V) sum = vf_piece<E, VEC>(p, q, hot, static_cast<int>(v0), static_cast<int>(min(v0 + prm.piece, static_cast<long long>(V))));
     sum = vf_warp_sum(sum);
     if (lane == 0) s_sum[warp] = sum;
     cluster.sync();
-    // every warp finds the piece: lanes scan the sums, 32 at a time
-    double total = 0.0;
-    for (int i0 = 0; i0 < pieces; i0 += 32) {
-      const int i = i0 + lane;
-      double x = 0.0;
-      if (i < pieces) x = *cluster.map_shared_rank(&s_sum[i % kVfWarps], i / kVfWarps);
-      total += vf_warp_sum(x);
+    // every warp scans the sums of all pieces, lane l those of pieces l per .. l per + per - 1
+    double x[4], own = 0.0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = lane * per + k;
+      x[k] = k < per && i < pieces ? *cluster.map_shared_rank(&s_sum[i % kVfWarps], i / kVfWarps) : 0.0;
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) own += x[k];
+    const double incl = vf_warp_scan(own);
+    const double total = __shfl_sync(0xffffffffu, incl, 31);
     if (!(total > 0.0)) {
       // nothing is left of p - q (p <= q everywhere): sample p itself; p without mass: no token
       if (!minus) {
@@ -144,41 +209,52 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
         break;
       }
       minus = false;
+      q = nullptr;
+      hot = -1;
       cluster.sync();                         // the sums are read before they are written again
       continue;
     }
     const double target = static_cast<double>(__ldg(u + T)) * total;
-    double before = 0.0, run = 0.0;
-    int found = -1, last = -1;
-    double last_before = 0.0;
-    for (int i0 = 0; i0 < pieces && found < 0; i0 += 32) {
-      const int i = i0 + lane;
-      double x = 0.0;
-      if (i < pieces) x = *cluster.map_shared_rank(&s_sum[i % kVfWarps], i / kVfWarps);
-      const double incl = vf_warp_scan(x);
-      const unsigned hit = __ballot_sync(0xffffffffu, x > 0.0 && run + incl > target);
-      const unsigned some = __ballot_sync(0xffffffffu, x > 0.0);
-      const double excl = run + (incl - x);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        found = i0 + l;
-        before = __shfl_sync(0xffffffffu, excl, l);
-      } else if (some) {
-        const int l = 31 - __clz(some);
-        last = i0 + l;
-        last_before = __shfl_sync(0xffffffffu, excl, l);
+    // the first piece whose running sum passes the target; if none does (u = 1, or the last
+    // rounding), the last piece with mass
+    const unsigned hit = __ballot_sync(0xffffffffu, own > 0.0 && incl > target);
+    const unsigned some = __ballot_sync(0xffffffffu, own > 0.0);
+    const int l = hit ? __ffs(hit) - 1 : 31 - __clz(some);
+    int found = -1;
+    double before = incl - own;
+    {
+      double at = before;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool passes = x[k] > 0.0 && (found < 0 || !hit) && (!hit || at + x[k] > target);
+        if (passes) {
+          found = lane * per + k;
+          before = at;
+        }
+        at += x[k];
       }
-      run += __shfl_sync(0xffffffffu, incl, 31);
+      if (hit && found < 0) {                 // the lane's own rounding: its last piece with mass
+        at = incl - own;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (x[k] > 0.0) {
+            found = lane * per + k;
+            before = at;
+          }
+          at += x[k];
+        }
+      }
     }
-    if (found < 0) {                          // u = 1, or the sum's last rounding: the last piece with mass
-      found = last;
-      before = last_before;
-    }
+    found = __shfl_sync(0xffffffffu, found, l);
+    before = __shfl_sync(0xffffffffu, before, l);
     if (found / kVfWarps == rank) {
       // this CTA holds the piece: each thread takes a contiguous share of it
       const long long w0 = static_cast<long long>(found) * prm.piece;
       const int len = static_cast<int>(min(static_cast<long long>(prm.piece), V - w0));
       const int share = (len + kVfThreads - 1) / kVfThreads;
+      auto weight = [&](int v) -> double {
+        return vf_weight(vf_load(p + v), v == hot ? 1.f : (q ? vf_load(q + v) : 0.f));
+      };
       const int e0 = min(tid * share, len), e1 = min(e0 + share, len);
       double own = 0.0;
       int top = -1;                           // last token of the share with mass

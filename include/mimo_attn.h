@@ -327,7 +327,8 @@ mimo_status mimo_attn_prefill_first(const mimo_shape* shape, const void* q, cons
  *  max_pages          entries per sequence; max_pages * page_size < 2^31
  *  num_pages          pages in the pool
  *  page_size          tokens per page, any size >= 1
- *  page_stride_tokens distance between pages in tokens (>= page_size), the same for K, V and scales
+ *  page_stride_tokens distance between pages in tokens (>= page_size), the same for K, V and scales;
+ *                     num_pages * page_stride_tokens * Hkv < 2^31
  */
 typedef struct mimo_pages {
   const int* block_table;
