@@ -498,7 +498,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // epilogue: o = O / l -> bf16, lse = (m + log2 l) ln 2
       if (!wait_all(bar(kBarPVDone), (it_kv + T - 1) & 1)) { ok = false; break; }
       tc_fence_after();
-      const float inv_l = l > 0.f ? 1.f / l : 0.f;
+      const bool none = FIRST ? l == 0.f : !(l > 0.f);   // no key and no sink (FIRST: a NaN stays one)
+      const float inv_l = none ? 0.f : 1.f / l;
       __nv_bfloat16* orow = p.out + ((static_cast<long long>(b) * p.n + qi) * p.Hq + h) * 128;
 #pragma unroll 1
       for (int cb = 0; cb < 8; ++cb) {
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       if (row_ok && p.lse)
         p.lse[(static_cast<long long>(b) * p.Hq + h) * p.n + qi] =
-            l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            none ? -INFINITY : (m + log2f(l)) * kLn2;
       tc_fence_before();
       it_kv += T;
     }

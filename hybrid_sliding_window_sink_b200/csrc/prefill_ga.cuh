@@ -634,7 +634,8 @@ __global__ void __launch_bounds__(kGaThreads, 1)
       // epilogue after the item's last PV: o = O / l, lse = (m + log2 l) ln 2
       if (!wait_all(bar(kGaPVDone + grp), (gt - 1) & 1)) { ok = false; break; }
       tc_fence_after();
-      const float inv_l = l > 0.f ? 1.f / l : 0.f;
+      const bool none = WIN ? l == 0.f : !(l > 0.f);   // no key and no sink (WIN: a NaN stays one)
+      const float inv_l = none ? 0.f : 1.f / l;
       __nv_bfloat16* orow = p.out + ((static_cast<long long>(b) * p.n + qi) * p.Hq + hq) * 128;
 #pragma unroll 1
       for (int c = 0; c < 8; c += 2) {
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(kGaThreads, 1)
       }
       if (row_ok && p.lse)
         p.lse[(static_cast<long long>(b) * p.Hq + hq) * p.n + qi] =
-            l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            none ? -INFINITY : (m + log2f(l)) * kLn2;
       tc_fence_before();
     }
   }

@@ -572,44 +572,11 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       if (!wait_all(bar(kSwSFull + w), (i >> 1) & 1)) break;
       tc_fence_after();
       if (ctid == 0) SWA_TRACE(i, 3);
-      // pass 1: row max over the valid keys (four slot blocks per TMEM round trip)
-      float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll 1
-      for (int c = 0; c < L::UNITS; c += 2) {
-        uint32_t v[2][16];
-        int elo[2], ehi[2], k[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          k[q] = c + q < L::UNITS ? block_class(c + q, elo[q], ehi[q]) : 0;
-          if (k[q]) tmem_ld16(trow + (c + q) * 16, v[q]);
-        }
-        tmem_wait_ld();
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float mq = -INFINITY;
-          if (k[q] == 2) {
-            float mb = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              mq = fmax3_v(mq, __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
-              mb = fmax3_v(mb, __uint_as_float(v[q][e + 2]), __uint_as_float(v[q][e + 3]));
-            }
-            mq = fmaxf(mq, mb);
-          } else if (k[q] == 1) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (e >= elo[q] && e <= ehi[q]) mq = fmaxf(mq, __uint_as_float(v[q][e]));
-          }
-          if (q & 1) mx1 = fmaxf(mx1, mq); else mx0 = fmaxf(mx0, mq);
-        }
-      }
-      const float mx = fmaxf(mx0, mx1);
-      const float amax = mx * p.scale_log2;                 // -inf when the row has no key
-      const float ref = amax == -INFINITY ? 0.f : amax;
-      // pass 2: P = exp2(a - amax) (0 outside the window), packed f16 into the S columns
+      float ref = 0.f;                                      // reference of P (log2 units)
       float sum0 = 0.f, sum1 = 0.f;
       // P of one slot block into pk; returns its sum
-      const unsigned long long sc2 = f2_pack(p.scale_log2, p.scale_log2), nref2 = f2_pack(-ref, -ref);
+      const unsigned long long sc2 = f2_pack(p.scale_log2, p.scale_log2);
+      unsigned long long nref2 = 0;
       auto p_block = [&](const uint32_t (&v)[16], int k, int elo, int ehi, uint32_t (&pk)[8]) -> float {
         if (k == 0) {
 #pragma unroll
@@ -632,23 +599,135 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         const float2 sab = f2_unpack(acc);
         return sab.x + sab.y;
       };
+      if constexpr (FIRST) {
+        // One pass. The reference is the maximum of the first two slot blocks that hold a key of the
+        // row, and moves only when a later pair lies 2^8 above it (the P written so far are then
+        // scaled, a power of two at a time, so exactly; rare). P = 2^(a - ref) stays within 2^8 of 1
+        // at its largest, which f16 carries with all its 11 bits. Saves the six TMEM round trips of a
+        // separate maximum: n = 32768, 64/8 heads 553 -> ONEPASS us.
+        ref = -INFINITY;
 #pragma unroll 1
-      for (int c = 0; c < L::UNITS; c += 2) {
-        uint32_t v[2][16];
-        int elo[2], ehi[2], k[2];
+        for (int c = 0; c < L::UNITS; c += 2) {
+          uint32_t v[2][16];
+          int elo[2], ehi[2], k[2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          k[q] = c + q < L::UNITS ? block_class(c + q, elo[q], ehi[q]) : 0;
-          if (k[q]) tmem_ld16(trow + (c + q) * 16, v[q]);
-        }
-        tmem_wait_ld();
+          for (int q = 0; q < 2; ++q) {
+            k[q] = block_class(c + q, elo[q], ehi[q]);
+            if (k[q]) tmem_ld16(trow + (c + q) * 16, v[q]);
+          }
+          tmem_wait_ld();
+          float pm = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (c + q < L::UNITS) {
+          for (int q = 0; q < 2; ++q) {
+            float mq = -INFINITY, mb = -INFINITY;
+            if (k[q] == 2) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                mq = fmax3_v(mq, __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
+                mb = fmax3_v(mb, __uint_as_float(v[q][e + 2]), __uint_as_float(v[q][e + 3]));
+              }
+            } else if (k[q] == 1) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (e >= elo[q] && e <= ehi[q]) mq = fmaxf(mq, __uint_as_float(v[q][e]));
+            }
+            pm = fmax3(pm, mq, mb);
+          }
+          pm *= p.scale_log2;
+          const bool move = pm > ref + 8.f;                 // (also the first key of the row)
+          if (__any_sync(0xffffffffu, move)) {
+            const float to = move ? ceilf(pm) : ref;        // whole steps: scaling P is exact
+            const float al = move && ref != -INFINITY ? ex2(ref - to) : 1.f;
+            ref = to;
+            if (__any_sync(0xffffffffu, al != 1.f)) {
+              sum0 *= al;
+              sum1 *= al;
+              const __half2 al2 = __float2half2_rn(al);
+              tmem_wait_st();
+#pragma unroll 1
+              for (int c2 = 0; c2 < c; c2 += 2) {
+                uint32_t w[16];
+                tmem_ld16(trow + c2 * 8, w);
+                tmem_wait_ld();
+                uint32_t lo[8], hi[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&w[e]), al2);
+                  const __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&w[8 + e]), al2);
+                  lo[e] = *reinterpret_cast<const uint32_t*>(&a);
+                  hi[e] = *reinterpret_cast<const uint32_t*>(&b);
+                }
+                tmem_st8(trow + c2 * 8, lo);
+                tmem_st8(trow + c2 * 8 + 8, hi);
+              }
+            }
+          }
+          const float r0 = ref == -INFINITY ? 0.f : ref;
+          nref2 = f2_pack(-r0, -r0);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
             uint32_t pk[8];
             const float sq = p_block(v[q], k[q], elo[q], ehi[q], pk);
             if (q & 1) sum1 += sq; else sum0 += sq;
             tmem_st8(trow + (c + q) * 8, pk);
+          }
+        }
+        ref = ref == -INFINITY ? 0.f : ref;                 // a row without keys
+      } else {
+        // pass 1: row max over the valid keys (four slot blocks per TMEM round trip)
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < L::UNITS; c += 2) {
+          uint32_t v[2][16];
+          int elo[2], ehi[2], k[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            k[q] = c + q < L::UNITS ? block_class(c + q, elo[q], ehi[q]) : 0;
+            if (k[q]) tmem_ld16(trow + (c + q) * 16, v[q]);
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float mq = -INFINITY;
+            if (k[q] == 2) {
+              float mb = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                mq = fmax3_v(mq, __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
+                mb = fmax3_v(mb, __uint_as_float(v[q][e + 2]), __uint_as_float(v[q][e + 3]));
+              }
+              mq = fmaxf(mq, mb);
+            } else if (k[q] == 1) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (e >= elo[q] && e <= ehi[q]) mq = fmaxf(mq, __uint_as_float(v[q][e]));
+            }
+            if (q & 1) mx1 = fmaxf(mx1, mq); else mx0 = fmaxf(mx0, mq);
+          }
+        }
+        const float mx = fmaxf(mx0, mx1);
+        const float amax = mx * p.scale_log2;                 // -inf when the row has no key
+        ref = amax == -INFINITY ? 0.f : amax;
+        nref2 = f2_pack(-ref, -ref);
+        // pass 2: P = exp2(a - amax) (0 outside the window), packed f16 into the S columns
+#pragma unroll 1
+        for (int c = 0; c < L::UNITS; c += 2) {
+          uint32_t v[2][16];
+          int elo[2], ehi[2], k[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            k[q] = c + q < L::UNITS ? block_class(c + q, elo[q], ehi[q]) : 0;
+            if (k[q]) tmem_ld16(trow + (c + q) * 16, v[q]);
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (c + q < L::UNITS) {
+              uint32_t pk[8];
+              const float sq = p_block(v[q], k[q], elo[q], ehi[q], pk);
+              if (q & 1) sum1 += sq; else sum0 += sq;
+              tmem_st8(trow + (c + q) * 8, pk);
+            }
           }
         }
       }
@@ -666,7 +745,8 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       if (!wait_all(bar(kSwPVDone + w), (i >> 1) & 1)) break;
       tc_fence_after();
       if (ctid == 0) SWA_TRACE(i, 5);
-      const float inv_l = lt > 0.f ? sc / lt : 0.f;
+      const bool none = FIRST ? lt == 0.f : !(lt > 0.f);   // no key and no sink (FIRST: a NaN stays one)
+      const float inv_l = none ? 0.f : sc / lt;
       __nv_bfloat16* orow = p.out + ((static_cast<long long>(b) * p.n + qi) * p.Hq + hq) * 128;
       // O columns [128, 192) overlap the S columns of this group's next tile: read them
       // first, release the TMEM region, then finish with columns [192, 256)
@@ -698,7 +778,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       }
       if (row_ok && p.lse)
         p.lse[(static_cast<long long>(b) * p.Hq + hq) * p.n + qi] =
-            lt > 0.f ? (M + log2f(lt)) * kLn2 : -INFINITY;
+            none ? -INFINITY : (M + log2f(lt)) * kLn2;
       if (ctid == 0) SWA_TRACE(i, 6);
     }
   }

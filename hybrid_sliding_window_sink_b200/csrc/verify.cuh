@@ -12,8 +12,8 @@
 //
 // Work: one row of p and one of q per sequence, read once (the accepted rows are only probed at
 // x_t), so the bytes bound it; for few sequences the latency of the steps does. A cluster of C
-// CTAs shares a row: warp k of the cluster's C * 16 sums one contiguous piece, the sums meet in
-// distributed shared memory, and the CTA of the piece that the target falls into reads that
+// CTAs shares a row: warp k of the cluster sums one contiguous piece and writes the sum into
+// every CTA's shared memory, and the CTA of the piece that the target falls into reads that
 // piece again (from L2) with all its threads to find the token.
 #pragma once
 
@@ -23,9 +23,11 @@
 
 namespace mimo {
 
-constexpr int kVfThreads = 512;
+constexpr int kVfThreads = 256;
 constexpr int kVfWarps = kVfThreads / 32;
-constexpr int kVfMaxCluster = 8;
+constexpr int kVfMaxCluster = 8;   // with 256 threads: 5.4 us for one row of 32000 and 17.6 us for 64 of
+                                    // 131072; 512 threads 6.4 and 22.0, 1024 threads in clusters of 4 9.2 and 26
+                                    // (fewer clusters are resident), clusters of 4 6.0 and 19.9
 
 struct VerifyParams {
   const void* p;              // [B, T + 1, V] fp32 or bf16
@@ -87,6 +89,25 @@ struct VfVec<__nv_bfloat16> {
   }
 };
 
+// A running sum of weights as two floats, s + c: the difference p - q (error e) and the addition
+// to s (its error) are split exactly, and c collects the errors. A lane adds some 100 weights, so
+// the sum is good to about 2^-43 of itself, where a token weighs 2^-17; converting every value to
+// double instead made the kernel 2.5 times slower (the conversions, at V = 131072).
+struct VfSum {
+  float s = 0.f, c = 0.f;
+  __device__ __forceinline__ void add(float p, float q) {
+    // the weights of vf_weight: p > q, both finite
+    const bool ok = p > q && p <= 3.402823466e38f && q >= -3.402823466e38f;
+    p = ok ? p : 0.f;
+    q = ok ? q : 0.f;
+    const float d = p - q, b = d - p, e = (p - (d - b)) - (q + b);
+    const float t = s + d, z = t - s;
+    c += ((s - (t - z)) + (d - z)) + e;
+    s = t;
+  }
+  __device__ __forceinline__ double get() const { return static_cast<double>(s) + static_cast<double>(c); }
+};
+
 // Sum of the weights of [v0, v1) by one warp (each lane returns its share). VEC: 16-byte loads,
 // which need rows that start on 16 bytes (V a multiple of W); otherwise one value per lane and
 // load, eight loads in flight.
@@ -94,7 +115,7 @@ template <typename E, bool VEC>
 __device__ __forceinline__ double vf_piece(const E* p, const E* q, int hot, int v0, int v1) {
   using X = VfVec<E>;
   const int lane = threadIdx.x & 31;
-  double sum = 0.0;
+  VfSum sum[2];
   if constexpr (VEC) {
     constexpr int W = X::W, U = X::U;
     for (int v = v0 + lane * W; v < v1; v += 32 * W * U) {
@@ -114,7 +135,7 @@ __device__ __forceinline__ double vf_piece(const E* p, const E* q, int hot, int 
         X::get(a[u], x);
         X::get(b[u], y);
 #pragma unroll
-        for (int e = 0; e < W; ++e) sum += vf_weight(x[e], v + u * 32 * W + e == hot ? 1.f : y[e]);
+        for (int e = 0; e < W; ++e) sum[e & 1].add(x[e], v + u * 32 * W + e == hot ? 1.f : y[e]);
       }
     }
   } else {
@@ -128,19 +149,22 @@ __device__ __forceinline__ double vf_piece(const E* p, const E* q, int hot, int 
         y[u] = at < v1 && q ? vf_load(q + at) : 0.f;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) sum += vf_weight(x[u], v + u * 32 == hot ? 1.f : y[u]);
+      for (int u = 0; u < U; ++u) sum[u & 1].add(x[u], v + u * 32 == hot ? 1.f : y[u]);
     }
   }
-  return sum;
+  return sum[0].get() + sum[1].get();
 }
+
+static_assert(kVfMaxCluster * kVfWarps <= 64, "two pieces a lane");
 
 template <typename E, bool VEC>
 __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams prm) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ double s_sum[kVfWarps];          // this CTA's piece sums (read by the cluster)
+  __shared__ double s_sum[kVfMaxCluster * kVfWarps];   // every piece's sum (written by the cluster)
   __shared__ double s_scan[kVfWarps];
   __shared__ int s_acc, s_found;
+  cluster.barrier_arrive();                   // every CTA has started (waited for before the first write)
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int T = prm.T, V = prm.V;
@@ -180,23 +204,26 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
   const E* q = prm.q && minus ? q0 + static_cast<long long>(a) * V : nullptr;
   int hot = minus && !prm.q ? __ldg(draft + a) : -1;
   const int pieces = C * kVfWarps, mine = rank * kVfWarps + warp;
-  const int per = (pieces + 31) / 32;         // pieces a lane scans (at most 4)
+  const int per = (pieces + 31) / 32;         // pieces a lane scans (at most 2)
+  bool started = false;
   for (;;) {
     const long long v0 = static_cast<long long>(mine) * prm.piece;
     double sum = 0.0;
     if (v0 < V) sum = vf_piece<E, VEC>(p, q, hot, static_cast<int>(v0), static_cast<int>(min(v0 + prm.piece, static_cast<long long>(V))));
     sum = vf_warp_sum(sum);
-    if (lane == 0) s_sum[warp] = sum;
+    if (!started) cluster.barrier_wait();
+    started = true;
+    if (lane < C) *cluster.map_shared_rank(&s_sum[mine], lane) = sum;
     cluster.sync();
     // every warp scans the sums of all pieces, lane l those of pieces l per .. l per + per - 1
-    double x[4], own = 0.0;
+    double x[2], own = 0.0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
       const int i = lane * per + k;
-      x[k] = k < per && i < pieces ? *cluster.map_shared_rank(&s_sum[i % kVfWarps], i / kVfWarps) : 0.0;
+      x[k] = k < per && i < pieces ? s_sum[i] : 0.0;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) own += x[k];
+    for (int k = 0; k < 2; ++k) own += x[k];
     const double incl = vf_warp_scan(own);
     const double total = __shfl_sync(0xffffffffu, incl, 31);
     if (!(total > 0.0)) {
@@ -225,7 +252,7 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
     {
       double at = before;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         const bool passes = x[k] > 0.0 && (found < 0 || !hit) && (!hit || at + x[k] > target);
         if (passes) {
           found = lane * per + k;
@@ -236,7 +263,7 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
       if (hit && found < 0) {                 // the lane's own rounding: its last piece with mass
         at = incl - own;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
           if (x[k] > 0.0) {
             found = lane * per + k;
             before = at;
@@ -247,43 +274,54 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
     }
     found = __shfl_sync(0xffffffffu, found, l);
     before = __shfl_sync(0xffffffffu, before, l);
-    if (found / kVfWarps == rank) {
-      // this CTA holds the piece: each thread takes a contiguous share of it
-      const long long w0 = static_cast<long long>(found) * prm.piece;
-      const int len = static_cast<int>(min(static_cast<long long>(prm.piece), V - w0));
-      const int share = (len + kVfThreads - 1) / kVfThreads;
-      auto weight = [&](int v) -> double {
-        return vf_weight(vf_load(p + v), v == hot ? 1.f : (q ? vf_load(q + v) : 0.f));
-      };
-      const int e0 = min(tid * share, len), e1 = min(e0 + share, len);
-      double own = 0.0;
-      int top = -1;                           // last token of the share with mass
-      for (int e = e0; e < e1; ++e) {
-        const double w = weight(static_cast<int>(w0) + e);
-        own += w;
-        if (w > 0.0) top = e;
-      }
-      const double incl = vf_warp_scan(own);
-      if (lane == 31) s_scan[warp] = incl;
+    if (found / kVfWarps == rank) {         // (the same for the whole CTA)
+      // this CTA holds the piece: four consecutive tokens a thread, and so on until the running
+      // sum passes the target (at the first round for a row of up to 2^17 tokens)
+      const int w0 = found * prm.piece;
+      const int end = static_cast<int>(min(static_cast<long long>(w0) + prm.piece, static_cast<long long>(V)));
       if (tid == 0) s_found = 0x7fffffff;
-      __syncthreads();
-      double at = before;
-      for (int w = 0; w < warp; ++w) at += s_scan[w];
-      at += incl - own;
-      int hit = 0x7fffffff;
-      for (int e = e0; e < e1; ++e) {
-        const double w = weight(static_cast<int>(w0) + e);
-        at += w;
-        if (w > 0.0 && at > target) {
-          hit = e;
-          break;
+      int top = -1;                           // this thread's last token with mass
+      for (int c0 = w0; c0 < end; c0 += 4 * kVfThreads) {
+        const int v0 = c0 + 4 * tid;
+        float pv[4], qv[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int v = v0 + k;
+          pv[k] = v < end ? vf_load(p + v) : 0.f;
+          qv[k] = v < end && q ? vf_load(q + v) : 0.f;
         }
+        double w[4], own = 0.0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          w[k] = vf_weight(pv[k], v0 + k == hot ? 1.f : qv[k]);
+          own += w[k];
+          if (w[k] > 0.0) top = v0 + k;
+        }
+        const double incl = vf_warp_scan(own);
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        double at = before, all = before;
+#pragma unroll
+        for (int i = 0; i < kVfWarps; ++i) {
+          if (i < warp) at += s_scan[i];
+          all += s_scan[i];
+        }
+        at += incl - own;
+        int hit = 0x7fffffff;
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          double upto = at;
+          for (int k2 = 0; k2 <= k; ++k2) upto += w[k2];
+          if (w[k] > 0.0 && upto > target) hit = v0 + k;
+        }
+        hit = __reduce_min_sync(0xffffffffu, hit);
+        if (lane == 0 && hit != 0x7fffffff) atomicMin(&s_found, hit);
+        __syncthreads();
+        before = all;
+        if (s_found != 0x7fffffff) break;
       }
-      if (hit != 0x7fffffff) atomicMin(&s_found, hit);
-      __syncthreads();
-      const bool none = s_found == 0x7fffffff;
-      __syncthreads();
-      if (none) {                             // the last rounding again: the piece's last token with mass
+      if (s_found == 0x7fffffff) {            // the last rounding again: the piece's last token with mass
+        __syncthreads();
         if (tid == 0) s_found = -1;
         __syncthreads();
         if (top >= 0) atomicMax(&s_found, top);
@@ -291,7 +329,7 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
       }
       if (tid == 0) {
         prm.accepted[b] = a;
-        prm.tokens[static_cast<long long>(b) * (T + 1) + a] = static_cast<int>(w0) + s_found;
+        prm.tokens[static_cast<long long>(b) * (T + 1) + a] = s_found;
       }
     }
     break;
@@ -300,7 +338,6 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
     for (int t = tid; t <= T; t += kVfThreads)
       if (t != a) prm.tokens[static_cast<long long>(b) * (T + 1) + t] = t < a ? __ldg(draft + t) : -1;
   }
-  cluster.sync();                             // no CTA leaves while its sums may be read
 }
 
 }  // namespace mimo

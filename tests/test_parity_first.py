@@ -185,3 +185,29 @@ def test_values_that_are_not_finite_stay_where_they_are_seen(cuda_device, hq, hk
         for t in at:
             sees = [i for i in range(t, 385) if t > i - window or t < first]
             assert np.isnan(got[0, sees, :hq // hkv, t % 128]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,window,first", [(8, 1, 128, 4), (8, 1, 200, 40), (4, 2, 128, 4)])
+def test_a_nan_score_shows(cuda_device, hq, hkv, window, first):
+    inp = _inputs(1, 300, 0, hq, hkv, 71)
+    inp["k"][0, 20, 0, 100] = float("nan")
+    d = {k: v.to(cuda_device) for k, v in inp.items()}
+    out, lse = _lib.prefill_first(d["q"], d["k"], d["v"], d["sink"], window=window, n_first=first)
+    torch.cuda.synchronize()
+    sees = torch.tensor([20 <= i < 20 + window or (i >= 20 and 20 < first) for i in range(300)])
+    G = hq // hkv
+    assert torch.isnan(out[0, sees, :G]).all() and torch.isnan(lse[0, :G, sees]).all()
+    assert torch.isfinite(out[0, ~sees]).all() and torch.isfinite(lse[0][:, ~sees]).all()
+
+
+@pytest.mark.gpu
+def test_scores_that_rise_along_the_window(cuda_device):
+    """Keys whose scores climb by far more than 2^8 from slot to slot, so that references move."""
+    inp = _inputs(1, 420, 0, 8, 1, 72)
+    ramp = torch.linspace(0, 30, 420)[None, :, None]
+    for sign in (1, -1):
+        inp["k"][..., 64] = (ramp * sign).bfloat16()
+        inp["q"][..., 64] = 20.0
+        for window, first in ((128, 4), (160, 30)):
+            _check(inp, cuda_device, window, first, rot=64, what=f"ramp {sign}")
