@@ -62,6 +62,15 @@ struct PrefillParams {
   unsigned long long* trace;   // debug timestamps (builds with -DMIMO_TRACE only), else null
 };
 
+// Placed right after tmem_wait_ld(): makes every later use of r depend on this point, so
+// the compiler cannot move arithmetic on TMEM-loaded registers above the wait.
+__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
 template <int G, int BN, int NKS>
 struct PfCfg {
   static constexpr int P = 128 / G;

@@ -56,14 +56,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r));
   tmem_ld16(taddr + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
 }
-// Placed right after tmem_wait_ld(): makes every later use of r depend on this point, so
-// the compiler cannot move arithmetic on TMEM-loaded registers above the wait.
-__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
-  asm volatile(""
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
-}
 __device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
   reg_fence16(*reinterpret_cast<uint32_t(*)[16]>(r));
   reg_fence16(*reinterpret_cast<uint32_t(*)[16]>(r + 16));

@@ -365,18 +365,22 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
             tc_fence_after();
             const int uq = useq_of[npv & 3];
             const uint32_t base = tmem + wg * 256;
+            if constexpr (FIRST) {
+              // the first tokens' unit, then the nine of the window; not the two slots outside it: they
+              // may be taking rows of later keys, which are not f16 yet (and may hold anything)
+              umma_ts(base + 128, base + 8 * kSwaUnits, smem_desc(sV + kSwaUnits * L::UNIT_BYTES, L::R_CHUNK, 1024),
+                      L::IDESC_PV, 0u);
+              const int um = uq % kSwaUnits;
+              const uint32_t out2 = (1u << (um + 1 < kSwaUnits ? um + 1 : um + 1 - kSwaUnits)) |
+                                    (1u << (um + 2 < kSwaUnits ? um + 2 : um + 2 - kSwaUnits));
 #pragma unroll
-            for (int s2 = 0; s2 < L::UNITS; ++s2) {
-              const uint64_t bd = smem_desc(sV + s2 * L::UNIT_BYTES, L::R_CHUNK, 1024);
-              if constexpr (FIRST) {
-                // not the two slots outside the window: they may be taking rows of later keys, which
-                // are not f16 yet (and may hold anything). The first unit is always in, and first.
-                const int u2 = s2 == 0 ? kSwaUnits : s2 - 1;
-                const int back = uq % kSwaUnits - u2;
-                if (s2 > 0 && (back < 0 ? back + kSwaUnits : back) >= kSwaWin) continue;
-                umma_ts(base + 128, base + 8 * u2, smem_desc(sV + u2 * L::UNIT_BYTES, L::R_CHUNK, 1024), L::IDESC_PV,
-                        s2 > 0 ? 1u : 0u);
-              } else {
+              for (int s2 = 0; s2 < kSwaUnits; ++s2)
+                if (!(out2 >> s2 & 1u))
+                  umma_ts(base + 128, base + 8 * s2, smem_desc(sV + s2 * L::UNIT_BYTES, L::R_CHUNK, 1024), L::IDESC_PV, 1u);
+            } else {
+#pragma unroll
+              for (int s2 = 0; s2 < kSwaUnits; ++s2) {
+                const uint64_t bd = smem_desc(sV + s2 * L::UNIT_BYTES, L::R_CHUNK, 1024);
                 umma_ts(base + 128, base + 8 * s2, bd, L::IDESC_PV, s2 > 0 ? 1u : 0u);
               }
             }
@@ -449,6 +453,15 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
             make_uint4(bf16x2_to_f16x2(xv[h2].x), bf16x2_to_f16x2(xv[h2].y),
                        bf16x2_to_f16x2(xv[h2].z), bf16x2_to_f16x2(xv[h2].w));
     };
+    float2 turn[4];   // (FIRST) (cos, sin)(j w_lane) of positions j = warp, warp + 4, .. of a block
+    if (FIRST && half == 32) {
+#pragma unroll
+      for (int i2 = 0; i2 < 4; ++i2) {
+        const double ang = static_cast<double>((ctid >> 5) + 4 * i2) * s_invf[lane];
+        const double nrev = rint(ang * 0.15915494309189535);
+        sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &turn[i2].y, &turn[i2].x);
+      }
+    }
     int seq = 0, i = 0, runs = 0;
     for (long long f = f0; f < f1; ++f, ++i) {
       const int t = static_cast<int>(f % nqt);
@@ -459,7 +472,19 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       float* tab = reinterpret_cast<float*>(smem + L::OFF_TAB + (i & 1) * L::TAB_BYTES);
       if (ctid == 0) SWA_TRACE(i, 0);
       // (cos, sin) of the block's 16 positions (double buffered: tile i - 1 may still read)
-      if (half > 0) {
+      if (FIRST && half == 32) {
+        // one angle per thread (frequency = lane), turned by the four positions the thread serves
+        const double ang = static_cast<double>(p0) * s_invf[lane];
+        const double nrev = rint(ang * 0.15915494309189535);
+        float sn, cs;
+        __sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &sn, &cs);
+#pragma unroll
+        for (int i2 = 0; i2 < 4; ++i2) {
+          float* tk = tab + ((ctid >> 5) + 4 * i2) * 64 + (lane >> 1) * 4 + (lane & 1);
+          tk[0] = cs * turn[i2].x - sn * turn[i2].y;
+          tk[2] = sn * turn[i2].x + cs * turn[i2].y;
+        }
+      } else if (half > 0) {
         for (int e = ctid; e < kSwaP * half; e += 128) {
           const int pp = e / half, k = e - pp * half;
           const double ang = static_cast<double>(p0 + pp) * s_invf[k];
@@ -470,6 +495,8 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
           tk[0] = cs;
           tk[2] = sn;
         }
+      }
+      if (half > 0) {
         mbar_arrive(bar(kSwTab + (i & 1)));   // (bounded waits only: no hardware named barrier)
         if (!wait_all(bar(kSwTab + (i & 1)), (i >> 1) & 1)) break;
       }
@@ -600,77 +627,80 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         return sab.x + sab.y;
       };
       if constexpr (FIRST) {
-        // One pass. The reference is the maximum of the first two slot blocks that hold a key of the
-        // row, and moves only when a later pair lies 2^8 above it (the P written so far are then
-        // scaled, a power of two at a time, so exactly; rare). P = 2^(a - ref) stays within 2^8 of 1
-        // at its largest, which f16 carries with all its 11 bits. Saves the six TMEM round trips of a
-        // separate maximum: n = 32768, 64/8 heads 553 -> ONEPASS us.
+        // One pass over the slot blocks, one block per turn. The reference is the maximum of the first
+        // block that holds a key of the row, rounded up to a whole step, and moves only when a later
+        // block lies 2^8 above it (the P written so far are then scaled by a power of two, so exactly;
+        // rare). P = 2^(a - ref) stays within 2^8 of 1 at its largest, which f16 carries with all its 11
+        // bits. A pass of its own for the maximum cost six TMEM round trips more; two blocks per turn, in
+        // variants for full and partial ones, more code than the instruction caches of an SM that runs
+        // four different roles hold (stalls for instructions doubled). n = 32768, 64/8 heads, one after
+        // the other under the power cap: two passes 553 us, pairs in one pass 573 (cold 515), with their
+        // loads ahead 620, this 461 (cold 411).
         ref = -INFINITY;
+        uint32_t v[16];
+        int elo, ehi;
+        tmem_ld16(trow, v);
 #pragma unroll 1
-        for (int c = 0; c < L::UNITS; c += 2) {
-          uint32_t v[2][16];
-          int elo[2], ehi[2], k[2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            k[q] = block_class(c + q, elo[q], ehi[q]);
-            if (k[q]) tmem_ld16(trow + (c + q) * 16, v[q]);
-          }
+        for (int c = 0; c < L::UNITS; ++c) {
           tmem_wait_ld();
-          float pm = -INFINITY;
+          reg_fence16(v);
+          float x[16];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float mq = -INFINITY, mb = -INFINITY;
-            if (k[q] == 2) {
-#pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                mq = fmax3_v(mq, __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
-                mb = fmax3_v(mb, __uint_as_float(v[q][e + 2]), __uint_as_float(v[q][e + 3]));
-              }
-            } else if (k[q] == 1) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (e >= elo[q] && e <= ehi[q]) mq = fmaxf(mq, __uint_as_float(v[q][e]));
-            }
-            pm = fmax3(pm, mq, mb);
+          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]);
+          // the next block's scores are under way while this one is worked on (P of block c ends at
+          // column 8 (c + 1), below them)
+          if (c + 1 < L::UNITS) tmem_ld16(trow + (c + 1) * 16, v);
+          const int kind = block_class(c, elo, ehi);
+          if (kind == 0) {                                  // no key for any row (the same for the tile)
+            const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+            tmem_st8(trow + c * 8, zero);
+            continue;
           }
-          pm *= p.scale_log2;
-          const bool move = pm > ref + 8.f;                 // (also the first key of the row)
-          if (__any_sync(0xffffffffu, move)) {
-            const float to = move ? ceilf(pm) : ref;        // whole steps: scaling P is exact
-            const float al = move && ref != -INFINITY ? ex2(ref - to) : 1.f;
-            ref = to;
-            if (__any_sync(0xffffffffu, al != 1.f)) {
-              sum0 *= al;
-              sum1 *= al;
-              const __half2 al2 = __float2half2_rn(al);
-              tmem_wait_st();
-#pragma unroll 1
-              for (int c2 = 0; c2 < c; c2 += 2) {
-                uint32_t w[16];
-                tmem_ld16(trow + c2 * 8, w);
-                tmem_wait_ld();
-                uint32_t lo[8], hi[8];
+          if (kind == 1) {                                  // masked keys to -inf
+            const uint32_t valid = ((1u << (ehi + 1)) - 1u) & ~((1u << elo) - 1u);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&w[e]), al2);
-                  const __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&w[8 + e]), al2);
-                  lo[e] = *reinterpret_cast<const uint32_t*>(&a);
-                  hi[e] = *reinterpret_cast<const uint32_t*>(&b);
-                }
-                tmem_st8(trow + c2 * 8, lo);
-                tmem_st8(trow + c2 * 8 + 8, hi);
+            for (int e = 0; e < 16; ++e) x[e] = valid >> e & 1u ? x[e] : -INFINITY;
+          }
+          float ma = fmax3(x[0], x[1], x[2]), mb = fmax3(x[3], x[4], x[5]);
+          ma = fmax3(ma, x[6], x[7]);
+          mb = fmax3(mb, x[8], x[9]);
+          ma = fmax3(ma, x[10], x[11]);
+          mb = fmax3(mb, x[12], x[13]);
+          const float pm = fmaxf(fmax3(ma, x[14], x[15]), mb) * p.scale_log2;
+          const bool move = pm > ref + 8.f;                 // (also the first key of the row)
+          const float was = ref;
+          ref = move ? ceilf(pm) : ref;                     // whole steps: scaling P is exact
+          if (__any_sync(0xffffffffu, move && was != -INFINITY)) {
+            const float al = move && was != -INFINITY ? ex2(was - ref) : 1.f;
+            sum0 *= al;
+            sum1 *= al;
+            const __half2 al2 = __float2half2_rn(al);
+            tmem_wait_st();
+#pragma unroll 1
+            for (int c2 = 0; c2 < c; ++c2) {
+              uint32_t w2[8];
+              tmem_ld8(trow + c2 * 8, w2);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&w2[e]), al2);
+                w2[e] = *reinterpret_cast<const uint32_t*>(&a);
               }
+              tmem_st8(trow + c2 * 8, w2);
             }
           }
           const float r0 = ref == -INFINITY ? 0.f : ref;
           nref2 = f2_pack(-r0, -r0);
+          uint32_t pk[8];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t pk[8];
-            const float sq = p_block(v[q], k[q], elo[q], ehi[q], pk);
-            if (q & 1) sum1 += sq; else sum0 += sq;
-            tmem_st8(trow + (c + q) * 8, pk);
+          for (int e = 0; e < 8; ++e) {
+            const float2 y = f2_unpack(f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), sc2, nref2));
+            const float a0 = ex2(y.x), a1 = ex2(y.y);
+            sum0 += a0;
+            sum1 += a1;
+            pk[e] = pack_f16(a0, a1);
           }
+          tmem_st8(trow + c * 8, pk);
         }
         ref = ref == -INFINITY ? 0.f : ref;                 // a row without keys
       } else {
