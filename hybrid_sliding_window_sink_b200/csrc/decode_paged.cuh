@@ -11,13 +11,13 @@
 // a table entry outside [0, num_pages) names no page and its tokens are masked keys.
 //
 // Split. The tiles of KT keys of all (sequence, KV head) units form one line, cut into as many
-// equal runs as there are CTAs (two per SM, all resident at once): lengths only exist on the
+// equal runs as there are CTAs (two per SM, four on FP8 pages, all resident at once): lengths only exist on the
 // device, so every CTA sums the units' tile counts itself and finds its run. A run that holds a
 // whole unit finishes it in place; at the ends of a run a unit's state (m, l, o) goes to a slot
 // of the workspace (two per CTA), and the combine kernel joins the slots of each cut unit with
 // the sink. Nothing depends on timing, so results repeat bit for bit.
 //
-// Tile. Rows arrive by 16-byte cp.async, kPgStages tiles in flight, without a pause where one
+// Tile. Rows arrive by 16-byte cp.async, NS tiles in flight, without a pause where one
 // unit ends and the next begins. Four warps share one softmax: warp w scores KT/4 of the keys
 // (S = Q K^T, m16n8k16 with the group's heads as rows), the weights P go to shared memory, and
 // warp w multiplies all of P with its 32 columns of V. So a warp holds 16 x 32 of O (16 registers
@@ -62,27 +62,32 @@ struct PagedParams {
 };
 
 constexpr int kPgThreads = 128;
-constexpr int kPgStages = 4;
 
 template <bool FP8>
 struct PagedCfg {
   static constexpr int KT = FP8 ? 64 : 32;                  // keys per tile
+  // CTAs per SM and stages. bf16 is bound by memory: 60 KB in flight per CTA. FP8 spends more
+  // instructions per byte (conversions, two references): more warps to hide them, and Q straight
+  // from memory instead of a buffer per stage (two sequences of 100-131k tokens: 60.5 us against
+  // 63.3 with two CTAs of four stages; bf16 with three CTAs of three stages: 65.8 against 63.9)
+  static constexpr int CTAS = FP8 ? 4 : 2;
+  static constexpr int NS = FP8 ? 2 : 4;
   static constexpr int KROW = FP8 ? kKRow8 : kKRow;         // bytes per K row
   static constexpr int VROW = FP8 ? kVRow8 : kVRow;
   static constexpr int TPR = FP8 ? 4 : 8;                   // threads per row while loading
   static constexpr int ROWS = KT / (kPgThreads / TPR);      // rows per thread (2)
   static constexpr int OFF_V = KT * KROW;
   static constexpr int OFF_Q = OFF_V + KT * VROW;           // a unit's 16 query rows (its first tile only)
-  static constexpr int OFF_OK = OFF_Q + 16 * kKRow;         // float [KT]: 0, or -inf: no cached token
+  static constexpr int OFF_OK = OFF_Q + (FP8 ? 0 : 16 * kKRow);   // float [KT]: 0, or -inf: no cached token
   static constexpr int OFF_SC = OFF_OK + KT * 4;            // float [2][KT] K and V scales
   static constexpr int STAGE = OFF_SC + (FP8 ? KT * 8 : 0);
   static constexpr int PROW = KT * 2 + 16;                  // bytes per row of P (padded: no bank conflicts)
-  static constexpr int OFF_P = kPgStages * STAGE;           // P high (or f16), then P low
+  static constexpr int OFF_P = NS * STAGE;           // P high (or f16), then P low
   static constexpr int OFF_MX = OFF_P + (FP8 ? 1 : 2) * 16 * PROW;   // float [2][16][4] row maxima per warp
   static constexpr int OFF_L = OFF_MX + 2 * 16 * 4 * 4;     // float [16][4] row sums per warp
   static constexpr int SMEM = OFF_L + 16 * 4 * 4;
   static_assert(ROWS == 2, "two rows per thread and tile");
-  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(CTAS * (SMEM + 1024 + 256) <= 228 * 1024, "CTAs per SM");
 };
 
 // The keys of sequence b: token of key t is t for t < nf, lo + t - nf above.
@@ -111,15 +116,20 @@ __device__ __forceinline__ uint32_t f16_bits(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// a / b for a >= 0, b > 0: the 64-bit division costs about 100 instructions more.
+__device__ __forceinline__ long long div_ll(long long a, int b) {
+  if (static_cast<unsigned long long>(a) >> 32) return a / b;
+  return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
 template <int KT>
 __device__ __forceinline__ int paged_tiles(int nkeys) {   // an empty unit keeps one (masked) tile
   return nkeys > 0 ? (nkeys - 1) / KT + 1 : 1;
 }
 
 template <int G, bool FP8>
-__global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kPgThreads, PagedCfg<FP8>::CTAS) decode_paged_kernel(const PagedParams p) {
   using C = PagedCfg<FP8>;
-  constexpr int KT = C::KT, NS = kPgStages;
+  constexpr int KT = C::KT, NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ long long s_scan[4];
   __shared__ int s_b0;
@@ -158,7 +168,10 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
     if (!by_unit && tid == 0 && p.hdr) p.hdr[cta] = make_int4(0, -1, -1, 0);
     return;
   }
-  const long long a = T * cta / N, e = T * (cta + 1) / N;
+  // tile T c / N as c (T div N) + c (T mod N) div N
+  const long long quo = div_ll(T, N);
+  const int rem = static_cast<int>(T - quo * N);
+  const long long a = quo * cta + rem * cta / N, e = quo * (cta + 1) + rem * (cta + 1) / N;
   {
     long long at = before + incl - mine;
     if (a >= at && a < at + mine) {
@@ -179,7 +192,7 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
   int lb = s_b0;
   PagedSeq ls = paged_seq(p, lb);
   int lt = paged_tiles<KT>(ls.nkeys);
-  int lg = static_cast<int>(s_off0 / lt), lj = static_cast<int>(s_off0 % lt);
+  int lg = static_cast<int>(div_ll(s_off0, lt)), lj = static_cast<int>(s_off0 - static_cast<long long>(lg) * lt);
   const int b0 = lb, g0 = lg, j0 = lj, t0 = lt;
   const int* tab = p.table + static_cast<long long>(lb) * p.max_pages;
   const int lrow = tid / C::TPR, lu = tid % C::TPR;
@@ -230,7 +243,7 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
       }
       if (lu == 0) *reinterpret_cast<float*>(smem + stage * C::STAGE + C::OFF_OK + row * 4) = ok ? 0.f : -INFINITY;
     }
-    if (unit_start) {                         // 16 rows of Q (zero above the group), swizzled
+    if (!FP8 && unit_start) {                 // 16 rows of Q (zero above the group), swizzled
       const uint8_t* qg = reinterpret_cast<const uint8_t*>(p.q + (static_cast<long long>(lb) * p.Hq + lg * G) * kDQK);
       for (int x = tid; x < 16 * 24; x += kPgThreads) {
         const int r = x / 24, u = x - r * 24;
@@ -298,20 +311,23 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
       fresh = false;
       if constexpr (FP8) {
         // k-slot order of a step (j, s): lane tq supplies dims 16 (4 j + tq) + 4 s .. + 3
+        const __nv_bfloat16* qg = p.q + (static_cast<long long>(cb) * p.Hq + cg * G) * kDQK;
 #pragma unroll
         for (int jj = 0; jj < 3; ++jj)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             const int r = gq + 8 * hh;
-            uint32_t w[8];
+            uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+            if (r < G) {
+              const uint4* src = reinterpret_cast<const uint4*>(qg + r * kDQK + 16 * (4 * jj + tq));
+              x0 = __ldg(src);
+              x1 = __ldg(src + 1);
+            }
+            const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-            for (int u2 = 0; u2 < 2; ++u2)
-              ld_shared_v4(sQ + r * kKRow + (((2 * (4 * jj + tq) + u2) ^ (r & 7)) << 4), w[4 * u2], w[4 * u2 + 1],
-                           w[4 * u2 + 2], w[4 * u2 + 3]);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              qa[4 * jj + s][hh] = pack_f16(bf16_lo(w[2 * s]), bf16_hi(w[2 * s]));
-              qa[4 * jj + s][2 + hh] = pack_f16(bf16_lo(w[2 * s + 1]), bf16_hi(w[2 * s + 1]));
+            for (int s4 = 0; s4 < 4; ++s4) {
+              qa[4 * jj + s4][hh] = pack_f16(bf16_lo(w[2 * s4]), bf16_hi(w[2 * s4]));
+              qa[4 * jj + s4][2 + hh] = pack_f16(bf16_lo(w[2 * s4 + 1]), bf16_hi(w[2 * s4 + 1]));
             }
           }
       } else {
@@ -584,7 +600,7 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
           // CTA c holds tiles [T c / N, T (c + 1) / N): the one with tile x is floor(((x + 1) N - 1) / T)
           const long long x = a + it + (ct - 1 - cj);
           h.y = cta;
-          h.z = static_cast<int>(((x + 1) * N - 1) / T);
+          h.z = static_cast<int>(((x + 1) * N - 1) / T);   // (once per CTA at most)
         }
         if (by_unit) {
           if (tid == 0) p.hdr[unit] = h;
@@ -610,27 +626,32 @@ __global__ void __launch_bounds__(kPgThreads, 2) decode_paged_kernel(const Paged
   if (!by_unit && tid == 0 && p.hdr) p.hdr[cta] = hdr;
 }
 
-// Joins the slots of one cut unit (blockIdx.x) for one query head of its group (blockIdx.y):
-// M = max(sink, max m_c), o = sum o_c 2^(m_c - M) / (2^(sink - M) + sum l_c 2^(m_c - M)). Warp w
-// takes slots w, w + 4, ..., eight of them (state and row together) in flight, under a running
-// maximum of its own: two trips to memory, the header's and the slots'.
-__global__ void __launch_bounds__(128) decode_paged_combine_kernel(const PagedParams p) {
+// Joins the slots of one cut unit (blockIdx.x) for 4 / WARPS query heads of its group
+// (blockIdx.y): M = max(sink, max m_c), o = sum o_c 2^(m_c - M) / (2^(sink - M) + sum l_c 2^(m_c - M)).
+// Warp w of a head's WARPS takes slots w, w + WARPS, ..., eight of them (state and row together) in
+// flight, under a running maximum of its own: two trips to memory, the header's and the slots'. Few
+// units are cut into many slots (four warps a head), many into two or three (one warp a head, so
+// that all blocks are resident when the main kernel ends).
+template <int WARPS>
+__global__ void __launch_bounds__(128) decode_paged_combine_kernel(const PagedParams p, int G) {
   __shared__ float4 s_o[4][32];
   __shared__ float2 s_ml[4];
   pdl_wait();
   pdl_trigger();
   const int4 h = p.hdr[blockIdx.x];
   if (h.y < 0) return;
-  const int G = gridDim.y, r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int block_warp = threadIdx.x >> 5, warp = block_warp % WARPS, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * (4 / WARPS) + block_warp / WARPS;
+  if (WARPS == 1 && r >= G) return;
   const int np = h.z - h.y + 1;
   float M = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = warp; i0 < np; i0 += 32) {
+  for (int i0 = warp; i0 < np; i0 += 8 * WARPS) {
     float2 ml[8];
     float4 x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int i = i0 + 4 * k;
+      const int i = i0 + WARPS * k;
       ml[k] = make_float2(-INFINITY, 0.f);
       x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < np) {
@@ -656,27 +677,35 @@ __global__ void __launch_bounds__(128) decode_paged_combine_kernel(const PagedPa
       acc.w += x[k].w * w;
     }
   }
-  s_o[warp][lane] = acc;
-  if (lane == 0) s_ml[warp] = make_float2(M, l);
-  __syncthreads();
-  if (warp != 0) return;
   const int b = h.x / p.Hkv, head = (h.x - b * p.Hkv) * G + r;
   const float sk = p.sink ? p.sink[head] * 1.4426950408889634f : -INFINITY;
-  float m = sk;
+  if constexpr (WARPS > 1) {
+    s_o[warp][lane] = acc;
+    if (lane == 0) s_ml[warp] = make_float2(M, l);
+    __syncthreads();
+    if (warp != 0) return;
+  }
+  float m = fmaxf(sk, M);
+  if constexpr (WARPS > 1) {
 #pragma unroll
-  for (int w = 0; w < 4; ++w) m = fmaxf(m, s_ml[w].x);
+    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_ml[w].x);
+  }
   const float ref = m == -INFINITY ? 0.f : m;
   float Lt = p.sink ? ex2(sk - ref) : 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float own = ex2(M - ref);
+  Lt += l * own;
+  acc.x *= own; acc.y *= own; acc.z *= own; acc.w *= own;
+  if constexpr (WARPS > 1) {
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = ex2(s_ml[w].x - ref);
-    const float4 x = s_o[w][lane];
-    Lt += s_ml[w].y * f;
-    acc.x += x.x * f;
-    acc.y += x.y * f;
-    acc.z += x.z * f;
-    acc.w += x.w * f;
+    for (int w = 1; w < WARPS; ++w) {
+      const float f = ex2(s_ml[w].x - ref);
+      const float4 x = s_o[w][lane];
+      Lt += s_ml[w].y * f;
+      acc.x += x.x * f;
+      acc.y += x.y * f;
+      acc.z += x.z * f;
+      acc.w += x.w * f;
+    }
   }
   const float f = Lt == 0.f ? 0.f : 1.f / Lt;
   const long long bh = static_cast<long long>(b) * p.Hq + head;

@@ -766,7 +766,7 @@ mimo_status check_pages(const mimo_pages* pg, int hkv) {
   return MIMO_OK;
 }
 
-// CTAs of the paged decode (two per SM, resident at once) and its workspace: headers of the
+// CTAs of the paged decode (all resident at once) and its workspace: headers of the
 // units that a run boundary cuts, then two slots of G rows per CTA.
 struct PagedPlan {
   int nctas;
@@ -783,7 +783,8 @@ PagedPlan plan_paged(const mimo_shape* s, const mimo_pages* pg, int window, int 
   if (window > 0) keys = std::min(keys, static_cast<long long>(window) + n_first);
   pl.split = keys > tile;
   const long long tiles = (keys + tile - 1) / tile;
-  pl.nctas = static_cast<int>(std::min<long long>(2LL * sms, U * tiles));
+  const long long ctas = fp8 ? mimo::PagedCfg<true>::CTAS : mimo::PagedCfg<false>::CTAS;
+  pl.nctas = static_cast<int>(std::min<long long>(ctas * sms, U * tiles));
   if (!pl.split) return pl;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = 2 * static_cast<size_t>(pl.nctas) * G;
@@ -802,10 +803,29 @@ mimo_status launch_paged(const mimo::PagedParams& prm, bool split, cudaStream_t 
     return MIMO_ERR_CUDA;
   }
   if (launch_pdl(kern, dim3(prm.nctas), mimo::kPgThreads, smem, st, prm, false) != cudaSuccess) return MIMO_ERR_CUDA;
+  if (!split) return MIMO_OK;
   const long long units = static_cast<long long>(prm.B) * prm.Hkv;
-  if (split && launch_pdl(mimo::decode_paged_combine_kernel,
-                          dim3(static_cast<unsigned>(std::min<long long>(units, prm.nctas)), G), 128, 0, st, prm) != cudaSuccess)
+  const unsigned cut = static_cast<unsigned>(std::min<long long>(units, prm.nctas));
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t err;
+  if (prm.nctas / units >= 8) {   // a unit is cut into that many slots or more
+    cfg.gridDim = dim3(cut, G);
+    err = cudaLaunchKernelEx(&cfg, mimo::decode_paged_combine_kernel<4>, prm, G);
+  } else {
+    cfg.gridDim = dim3(cut, (G + 3) / 4);
+    err = cudaLaunchKernelEx(&cfg, mimo::decode_paged_combine_kernel<1>, prm, G);
+  }
+  if (err != cudaSuccess) {
+    cudaGetLastError();
     return MIMO_ERR_CUDA;
+  }
   return MIMO_OK;
 }
 
