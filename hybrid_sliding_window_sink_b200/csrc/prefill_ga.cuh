@@ -102,6 +102,63 @@ enum : int {
   kGaNumBars = 24
 };
 
+// Bits 0 .. n - 1 (none for n <= 0, all 32 for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
+// Rotates dims [0, rot) (rot <= 64) of Q row `row` of a block in place, f16 (as rope_row). The G
+// neighbouring rows of one position share its angles: lane j of them computes the frequencies
+// j, j + G, .. and the others take (cos, sin) from it by shuffles, 32 / G sincos per row instead of
+// 32. Items of a window are short (18 tiles at W = 2048), and their first product waits for this.
+// Whole warps call it; `store` rows only are written.
+template <int G>
+__device__ __forceinline__ void rope_q_row(uint32_t base, int row, int pos, int rot, const double* invf, bool store) {
+  constexpr int N = 32 / G;                          // frequencies per lane
+  const int lane = threadIdx.x & 31, half = rot >> 1, nun = rot >> 4, j = lane % G;
+  float cs[N], sn[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+    if (j + G * i < half) {
+      const double ang = static_cast<double>(pos) * invf[j + G * i];
+      const double nrev = rint(ang * 0.15915494309189535);
+      __sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &sn[i], &cs[i]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (u >= nun) break;
+    const uint32_t a1 = base + row * 128 + ((u ^ (row & 7)) << 4);
+    const uint32_t a2 = base + row * 128 + (((u + nun) ^ (row & 7)) << 4);
+    uint32_t x[4], y[4];
+    ld_shared_v4(a1, x[0], x[1], x[2], x[3]);
+    ld_shared_v4(a2, y[0], y[1], y[2], y[3]);
+#pragma unroll
+    for (int e2 = 0; e2 < 4; ++e2) {
+      float r1[2], r2[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        constexpr int kSrc = G;
+        const int k = u * 8 + e2 * 2 + h;
+        const float c = __shfl_sync(0xffffffffu, cs[k / kSrc], (lane & ~(G - 1)) + k % kSrc);
+        const float s = __shfl_sync(0xffffffffu, sn[k / kSrc], (lane & ~(G - 1)) + k % kSrc);
+        const float v1 = h ? bf16_hi(x[e2]) : bf16_lo(x[e2]);
+        const float v2 = h ? bf16_hi(y[e2]) : bf16_lo(y[e2]);
+        r1[h] = v1 * c - v2 * s;
+        r2[h] = v2 * c + v1 * s;
+      }
+      x[e2] = pack_f16_sat(r1[0], r1[1]);
+      y[e2] = pack_f16_sat(r2[0], r2[1]);
+    }
+    if (store) {
+      st_shared_v4(a1, x[0], x[1], x[2], x[3]);
+      st_shared_v4(a2, y[0], y[1], y[2], y[3]);
+    }
+  }
+}
+
 template <int G, bool WIN = false>
 __global__ void __launch_bounds__(kGaThreads, 1)
     prefill_ga_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -387,8 +444,12 @@ __global__ void __launch_bounds__(kGaThreads, 1)
       if (half > 0) {
         for (int blk = 0; blk < 2; ++blk) {
           const int qi = p0 + blk * P + ctid / G;
-          if (qi < p.n)
-            rope_row(sQ + blk * L::Q_BLOCK, L::Q_CHUNK, ctid, p.q_off + qi, p.rot_dims, s_invf);
+          if constexpr (WIN) {
+            rope_q_row<G>(sQ + blk * L::Q_BLOCK, ctid, p.q_off + qi, p.rot_dims, s_invf, qi < p.n);
+          } else {
+            if (qi < p.n)
+              rope_row(sQ + blk * L::Q_BLOCK, L::Q_CHUNK, ctid, p.q_off + qi, p.rot_dims, s_invf);
+          }
         }
         fence_proxy_async_smem();
       }
@@ -514,6 +575,17 @@ __global__ void __launch_bounds__(kGaThreads, 1)
       const int hq = g * G + (r % G);
       const bool row_ok = qi < p.n;
       const float sink2 = p.sink ? p.sink[hq] * kLog2e : -INFINITY;
+      // (WIN) scores of columns kc .. kc + 63 that this row masks become -inf: one path through both
+      // passes for whole and partly masked tiles (their code lives in the instruction caches once)
+      auto mask_cols = [&](uint32_t (&v)[64], int kc) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k0 = kc + 32 * h;
+          const uint32_t valid = bits_below(pos + 1 - k0) & (~bits_below(pos - p.window + 1 - k0) | bits_below(p.n_first - k0));
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[32 * h + e] = valid >> e & 1u ? v[32 * h + e] : 0xff800000u;
+        }
+      };
       float m = sink2;                             // reference max (log2 units)
       float l = p.sink ? 1.f : 0.f;
       for (int j = 0; j < T; ++j, ++gt) {
@@ -533,7 +605,10 @@ __global__ void __launch_bounds__(kGaThreads, 1)
           tmem_wait_ld();
           reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(v));
           reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
-          if (full) {
+          if constexpr (WIN) {
+            if (!full) mask_cols(v, kt0 + c);
+          }
+          if (WIN || full) {
 #pragma unroll
             for (int e = 0; e < 64; e += 4) {
               mx0 = fmax3(mx0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
@@ -541,11 +616,10 @@ __global__ void __launch_bounds__(kGaThreads, 1)
             }
           } else {
             const int lim = pos - kt0 - c;   // columns e <= lim are keys <= pos
-            const int elo = lim - p.window + 1, ef = p.n_first - kt0 - c;   // (WIN) from elo on, or below ef
 #pragma unroll
             for (int e = 0; e < 64; e += 2) {
-              if (e <= lim && (!WIN || e >= elo || e < ef)) mx0 = fmaxf(mx0, __uint_as_float(v[e]));
-              if (e + 1 <= lim && (!WIN || e + 1 >= elo || e + 1 < ef)) mx1 = fmaxf(mx1, __uint_as_float(v[e + 1]));
+              if (e <= lim) mx0 = fmaxf(mx0, __uint_as_float(v[e]));
+              if (e + 1 <= lim) mx1 = fmaxf(mx1, __uint_as_float(v[e + 1]));
             }
           }
         }
@@ -589,7 +663,9 @@ __global__ void __launch_bounds__(kGaThreads, 1)
             reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(v));
             reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
             const int lim = pos - kt0 - c;   // columns e <= lim are keys <= pos
-            const int elo = lim - p.window + 1, ef = p.n_first - kt0 - c;   // (WIN) from elo on, or below ef
+            if constexpr (WIN) {
+              if (!full) mask_cols(v, kt0 + c);
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t pk[8];
@@ -600,8 +676,8 @@ __global__ void __launch_bounds__(kGaThreads, 1)
                 float a0 = ex2(y.x);
                 float a1 = ex2(y.y);
                 if (decltype(masked)::value) {
-                  a0 = col <= lim && (!WIN || col >= elo || col < ef) ? a0 : 0.f;
-                  a1 = col + 1 <= lim && (!WIN || col + 1 >= elo || col + 1 < ef) ? a1 : 0.f;
+                  a0 = col <= lim ? a0 : 0.f;
+                  a1 = col + 1 <= lim ? a1 : 0.f;
                 }
                 sab = f2_add(sab, f2_pack(a0, a1));
                 pk[e] = pack_bf16(a0, a1);
@@ -611,7 +687,7 @@ __global__ void __launch_bounds__(kGaThreads, 1)
             if (c == 0 && q4 == 0 && lane == 0) GA_TRACE(gt, 18 + grp);
           }
         };
-        if (full)
+        if (WIN || full)
           pass2(std::false_type{});
         else
           pass2(std::true_type{});
