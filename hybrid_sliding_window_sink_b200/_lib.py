@@ -57,6 +57,8 @@ class MimoPages(ctypes.Structure):
 
 
 _LIB = None
+_CALL = None      # _call.so bound to the library _CALL_LIB, or False when it has not been built
+_CALL_LIB = None
 
 
 def lib():
@@ -65,6 +67,26 @@ def lib():
     if _LIB is None:
         _LIB = load(LIB_PATH)
     return _LIB
+
+
+def _usual():
+    """The C++ marshalling of the usual calls (csrc/binding.cpp), bound to the library in use, or
+    False. Its functions return None for a call that is not usual, which the Python code then makes."""
+    global _CALL, _CALL_LIB
+    if _CALL_LIB is not _LIB or _LIB is None:
+        L = lib()
+        if _CALL is None:
+            try:
+                from . import _call as _CALL
+            except ImportError:
+                _CALL = False
+        if _CALL:
+            addresses = [ctypes.cast(getattr(L, "mimo_attn_" + f), ctypes.c_void_p).value for f in (
+                "prefill_first", "decode_paged", "decode_paged_fp8", "decode_paged_workspace_size",
+                "cache_append_paged", "cache_append_paged_fp8", "verify_drafts")]
+            _CALL.bind(*addresses)
+        _CALL_LIB = L
+    return _CALL
 
 
 def load(path):
@@ -435,7 +457,7 @@ class _On:
     """Makes device ``index`` current and yields the raw stream to launch on: the given stream
     (which must belong to that device), or the device's current one. Scratch and outputs
     allocated inside belong to that stream. Not used where the device is current already and no
-    stream is given (the usual call, see _usual)."""
+    stream is given (see _here)."""
 
     __slots__ = ("ctx", "index")
 
@@ -453,7 +475,7 @@ class _On:
         return self.ctx.__exit__(*exc)
 
 
-def _usual(index, stream):
+def _here(index, stream):
     return stream is None and index == torch.cuda.current_device()
 
 
@@ -492,6 +514,11 @@ def prefill_first(q, k, v, sink=None, *, window, n_first, pos_offset=0, k_prefix
     """mimo_attn_prefill_first. q [B,n,Hq,192] at positions pos_offset on; k, v [B,pos_offset+n,Hkv,·]
     (prefix K rotated when k_prefix_rotated). A query sees its last ``window`` tokens and the first
     ``n_first``. Returns (out [B,n,Hq,128] bf16, lse [B,Hq,n] fp32 or None)."""
+    if out is None and lse is None and stream is None and (call := _usual()):
+        got = call.prefill_first(q, k, v, sink, window, n_first, pos_offset, k_prefix_rotated, rope_theta, rot_dims,
+                                 softmax_scale, want_lse)
+        if got is not None:
+            return got
     dev = _cuda_device(q, "q")
     _need_at(q, "q", torch.bfloat16, (None, None, None, 192), dev)
     B, n, hq, _ = q.shape
@@ -513,7 +540,7 @@ def prefill_first(q, k, v, sink=None, *, window, n_first, pos_offset=0, k_prefix
             1 if k_prefix_rotated else 0, _addr(sink), window, n_first, rope_theta, rot_dims, o.data_ptr(), _addr(ls), st))
         return o, ls
 
-    if _usual(dev.index, stream):
+    if _here(dev.index, stream):
         return launch(_raw_stream(dev.index))
     with _On(dev.index, stream) as st:
         return launch(st)
@@ -583,6 +610,11 @@ def _paged_workspace(index, batch, hq, hkv, max_pages, page_size, window, n_firs
 
 def _decode_paged(q, k, v, scales, table, lengths, sink, window, n_first, softmax_scale, out, lse, want_lse,
                   workspace, stream):
+    if out is None and lse is None and workspace is None and stream is None and (call := _usual()):
+        ks, vs = (None, None) if scales is None else scales
+        got = call.decode_paged(q, k, v, ks, vs, table, lengths, sink, window, n_first, softmax_scale, want_lse)
+        if got is not None:
+            return got
     dev = _cuda_device(q, "q")
     _need_at(q, "q", torch.bfloat16, (None, None, 192), dev)
     B, hq, _ = q.shape
@@ -617,7 +649,7 @@ def _decode_paged(q, k, v, scales, table, lengths, sink, window, n_first, softma
                 lengths.data_ptr(), window, n_first, _addr(sink), o.data_ptr(), _addr(ls), _addr(ws), nbytes, st))
         return o, ls
 
-    if _usual(dev.index, stream):
+    if _here(dev.index, stream):
         return launch(_raw_stream(dev.index))
     with _On(dev.index, stream) as st:
         return launch(st)
@@ -647,6 +679,10 @@ def decode_paged_workspace_size(batch, hq, hkv, *, max_pages, page_size, window=
 
 
 def _append_paged(k_new, v_new, k, v, scales, table, positions, n_new, rope_theta, rot_dims, stream):
+    if stream is None and (call := _usual()):
+        ks, vs = (None, None) if scales is None else scales
+        if call.append_paged(k_new, v_new, k, v, ks, vs, table, positions, n_new, rope_theta, rot_dims):
+            return
     dev = _cuda_device(k_new, "k_new")
     _need_at(k_new, "k_new", torch.bfloat16, (None, None, None, 192), dev)
     B, n, hkv, _ = k_new.shape
@@ -669,7 +705,7 @@ def _append_paged(k_new, v_new, k, v, scales, table, positions, n_new, rope_thet
                 shape, k_new.data_ptr(), v_new.data_ptr(), positions.data_ptr(), _addr(n_new), rope_theta, rot_dims,
                 pages, k.data_ptr(), v.data_ptr(), scales[0].data_ptr(), scales[1].data_ptr(), st))
 
-    if _usual(dev.index, stream):
+    if _here(dev.index, stream):
         launch(_raw_stream(dev.index))
     else:
         with _On(dev.index, stream) as st:
@@ -698,6 +734,10 @@ def verify_drafts(target_probs, draft_tokens, uniforms, draft_probs=None, *, n_v
     """mimo_attn_verify_drafts. target_probs [B,T+1,V] fp32 or bf16, draft_tokens [B,T] int32, uniforms
     [B,T+1] fp32, draft_probs [B,T,V] (None: drafts by argmax), n_valid [B] int32 or None. Returns
     (n_accepted [B], tokens [B,T+1]) int32: the accepted drafts, the next token, then -1."""
+    if n_accepted is None and tokens is None and stream is None and (call := _usual()):
+        got = call.verify_drafts(target_probs, draft_tokens, uniforms, draft_probs, n_valid)
+        if got is not None:
+            return got
     dev = _cuda_device(target_probs, "target_probs")
     if target_probs.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"target_probs must be float32 or bfloat16, got {target_probs.dtype}")
@@ -725,7 +765,7 @@ def verify_drafts(target_probs, draft_tokens, uniforms, draft_probs=None, *, n_v
             draft_tokens.data_ptr(), uniforms.data_ptr(), _addr(n_valid), acc.data_ptr(), tok.data_ptr(), st))
         return acc, tok
 
-    if _usual(dev.index, stream):
+    if _here(dev.index, stream):
         return launch(_raw_stream(dev.index))
     with _On(dev.index, stream) as st:
         return launch(st)

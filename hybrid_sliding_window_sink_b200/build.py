@@ -76,8 +76,32 @@ def build(force: bool = False, verbose: bool = False, variant: str | None = None
     return path
 
 
+def build_binding(force: bool = False) -> str:
+    """Builds _call.so, the C++ marshalling of the usual calls (csrc/binding.cpp), against torch."""
+    path, src = os.path.join(PKG, "_call.so"), os.path.join(CSRC, "binding.cpp")
+    deps = [src, os.path.join(INCLUDE, "mimo_attn.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps):
+        return path
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-I", sysconfig.get_path("include"), "-isystem", os.path.join(cuda, "include")]
+    for d in cpp_extension.include_paths():
+        cmd += ["-isystem", d]
+    cmd += [src, "-o", path + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+    subprocess.run(cmd, check=True)
+    os.replace(path + ".tmp", path)
+    return path
+
+
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build_binding(force="--force" in sys.argv))
     if "--variants" in sys.argv:
         for name in VARIANTS:
             print(build(force="--force" in sys.argv, variant=name))

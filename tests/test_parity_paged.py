@@ -3,6 +3,8 @@
 Bounds (serve_util.check): P has 16 significant bits on bf16 pages (two bf16 terms: 2^-16 with the
 remainder's own rounding) and 11 on FP8 pages (f16 half step 2^-11)."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -412,3 +414,67 @@ def test_append_then_decode_in_a_graph(cuda_device):
         inp["lengths"] = torch.tensor([41 + t, 101 + t], dtype=torch.int32)
         o, l, mass, _ = _oracle(inp, 0, 0)
         check(out, lse, o, l, mass, 2.0 ** -16, score_error(wl.to_f64(inp["q"]), wl.to_f64(inp["k"]), SCALE), f"step {t}")
+
+
+@pytest.mark.gpu
+def test_the_two_marshallings_agree(cuda_device):
+    """The C++ marshalling is in place, and what it passes on (given outputs, another stream, refused
+    sizes) goes through Python with the same results."""
+    from hybrid_sliding_window_sink_b200 import _lib as lib
+    assert lib._usual(), "_call.so has not been built"
+    inp = to_dev(paged_inputs([300, 5, 0], 16, 2, 24, seed=42, page_gap=8), cuda_device)
+    args = [inp[x] for x in ("q", "k", "v", "table", "lengths", "sink")]
+    fast = lib._usual().decode_paged(args[0], args[1], args[2], None, None, *args[3:], 64, 3, 0.0, True)
+    out, lse = torch.empty_like(fast[0]), torch.empty_like(fast[1])
+    slow = _lib.decode_paged(*args, window=64, n_first=3, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert slow[0] is out and torch.equal(fast[0], out) and torch.equal(fast[1], lse)
+    none = lib._usual().decode_paged(args[0], args[1], args[2], None, None, *args[3:], 64, 3, 0.0, False)
+    assert none[1] is None
+    bad = [(0, args[0].float()), (0, args[0].cpu()), (1, args[1].transpose(1, 2)), (2, args[2][:, :10]), (3, args[3].long()),
+           (3, args[3][:2]), (4, args[4][:2]), (5, args[5].double()), (4, None), (1, None)]
+    for i, x in bad:
+        a = list(args)
+        a[i] = x
+        assert lib._usual().decode_paged(a[0], a[1], a[2], None, None, *a[3:], 64, 3, 0.0, True) is None, i
+        with pytest.raises((TypeError, ValueError)):
+            _lib.decode_paged(*a, window=64, n_first=3)
+    with pytest.raises(_lib.MimoError, match="SHAPE"):
+        _lib.decode_paged(*args, n_first=-1)
+    with pytest.raises((TypeError, ctypes.ArgumentError)):
+        _lib.decode_paged(*args, window="no")
+    with pytest.raises(TypeError):
+        lib._usual().decode_paged(1)
+
+
+@pytest.mark.gpu
+def test_bad_calls_of_the_other_operators(cuda_device):
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device=cuda_device)  # noqa: E731
+    i32 = torch.int32
+    k, v, t, p = z(3, 16, 2, 192), z(3, 16, 2, 128), z(1, 3, dtype=i32), z(1, dtype=i32)
+    kn, vn = z(1, 2, 2, 192), z(1, 2, 2, 128)
+    good = dict(k_new=kn, v_new=vn, k_pages=k, v_pages=v, block_table=t, positions=p)
+    for name, x in (("k_new", kn.float()), ("v_new", vn[:, :1]), ("k_pages", k[:, :, :1]), ("v_pages", v.cpu()),
+                    ("block_table", t.long()), ("positions", z(2, dtype=i32)), ("v_pages", v[:2])):
+        with pytest.raises((TypeError, ValueError)):
+            _lib.cache_append_paged(**{**good, name: x})
+    with pytest.raises(_lib.MimoError, match="UNSUPPORTED"):
+        _lib.cache_append_paged(**good, rot_dims=24)
+    with pytest.raises((TypeError, ValueError)):
+        _lib.cache_append_paged_fp8(kn, vn, k, v, z(3, 16, 2), z(3, 16, 2), t, p)
+    pr, d, u = z(2, 3, 50, dtype=torch.float32), z(2, 2, dtype=i32), z(2, 3, dtype=torch.float32)
+    for bad in ((pr.double(), d, u), (pr[0], d, u), (pr, d.long(), u), (pr, d, u[:, :2]), (pr, d, u.half()), (pr, d.cpu(), u)):
+        with pytest.raises((TypeError, ValueError)):
+            _lib.verify_drafts(*bad)
+    with pytest.raises((TypeError, ValueError)):
+        _lib.verify_drafts(pr, d, u, z(2, 2, 50))          # bf16 drafts beside fp32 targets
+    q, kk, vv = z(1, 5, 8, 192), z(1, 5, 1, 192), z(1, 5, 1, 128)
+    for bad in ((q, kk[:, :4], vv), (q, kk, vv.float()), (q.transpose(1, 2), kk, vv), (q, kk, vv, z(8))):
+        with pytest.raises((TypeError, ValueError)):
+            _lib.prefill_first(*bad, window=2, n_first=1)
+    with pytest.raises(_lib.MimoError, match="SHAPE"):
+        _lib.prefill_first(q, kk, vv, window=2, n_first=-1)
+    with pytest.raises(ValueError, match="stream"):
+        class Other:
+            device_index = 5
+        _lib.prefill_first(q, kk, vv, window=2, n_first=1, stream=Other())
