@@ -60,7 +60,9 @@ extern "C" void mimo_attn_debug_set_trace(void* p) { g_trace = static_cast<unsig
 namespace {
 
 using mimo::DecodeParams;
+using mimo::PrefillFirstParams;
 using mimo::PrefillParams;
+using mimo::PrefillParamsOf;
 
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_sm_count[kMaxDevices];
@@ -197,7 +199,7 @@ bool make_tmap(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint6
 // ---------------------------------------------------------------- prefill
 template <int G, int BN, int NKS, bool FIRST = false>
 mimo_status launch_prefill(const mimo_shape* s, const void* q, const void* k, const void* v,
-                           PrefillParams prm, int sms, cudaStream_t st) {
+                           PrefillParamsOf<FIRST> prm, int sms, cudaStream_t st) {
   using C = mimo::PfCfg<G, BN, NKS>;
   CUtensorMap tq, tk, tv;
   const uint64_t n = static_cast<uint64_t>(s->seqlen), B = static_cast<uint64_t>(s->batch);
@@ -223,7 +225,7 @@ mimo_status launch_prefill(const mimo_shape* s, const void* q, const void* k, co
 // SWA layer with 8 query heads per KV head, W <= 129, rot_dims <= 64: the ring kernel.
 template <bool FIRST = false>
 mimo_status launch_prefill_swa(const mimo_shape* s, const void* q, const void* k, const void* v,
-                               PrefillParams prm, int sms, cudaStream_t st) {
+                               PrefillParamsOf<FIRST> prm, int sms, cudaStream_t st) {
   using L = mimo::SwaLayout<FIRST>;
   CUtensorMap tq, tk, tv;
   const uint64_t n = static_cast<uint64_t>(s->seqlen), B = static_cast<uint64_t>(s->batch);
@@ -251,7 +253,7 @@ mimo_status launch_prefill_swa(const mimo_shape* s, const void* q, const void* k
 // two row blocks per work item share every K/V tile.
 template <int G, bool WIN = false>
 mimo_status launch_prefill_ga(const mimo_shape* s, const void* q, const void* k, const void* v,
-                              PrefillParams prm, int sms, cudaStream_t st) {
+                              PrefillParamsOf<WIN> prm, int sms, cudaStream_t st) {
   using L = mimo::GaLayout<G>;
   CUtensorMap tq, tk, tv;
   const uint64_t n = static_cast<uint64_t>(s->seqlen), B = static_cast<uint64_t>(s->batch);
@@ -311,7 +313,7 @@ mimo_status prefill_chunk_group(const mimo_shape* s, const void* q, const void* 
 // windows of 8 and 16 heads per KV head, the generic kernel for the rest.
 template <int G>
 mimo_status prefill_first_group(const mimo_shape* s, const void* q, const void* k, const void* v,
-                                const PrefillParams& prm, int sms, cudaStream_t st) {
+                                const PrefillFirstParams& prm, int sms, cudaStream_t st) {
   if (G == mimo::kSwaG && prm.window <= 129 && prm.n_first <= mimo::kSwaFirst && prm.rot_dims <= 64 &&
       prm.q_off % mimo::kSwaP == 0)
     return launch_prefill_swa<true>(s, q, k, v, prm, sms, st);
@@ -714,7 +716,7 @@ mimo_status run_prefill_chunk(const mimo_shape* s, const void* q, const void* k,
     return MIMO_ERR_ALIGN;
   const int dev = current_device();
   if (dev < 0) return MIMO_ERR_CUDA;
-  PrefillParams prm{};
+  PrefillFirstParams prm{};
   prm.sink = sink;
   prm.out = static_cast<__nv_bfloat16*>(out);
   prm.lse = lse;
@@ -738,6 +740,7 @@ mimo_status run_prefill_chunk(const mimo_shape* s, const void* q, const void* k,
   const int group = s->n_q_heads / s->n_kv_heads;
   // without a window that ends inside the keys, the first tokens are visible anyway
   if (n_first > 0 && window > 0 && window < prm.nk) {
+    for (int d = 0; d < rot_dims / 2; ++d) prm.invf[d] = std::pow(prm.rope_theta, -2.0 * d / rot_dims);
     switch (group) {
       case 1: return prefill_first_group<1>(s, q, k, v, prm, sms, st);
       case 2: return prefill_first_group<2>(s, q, k, v, prm, sms, st);

@@ -34,6 +34,8 @@
 // and the device error word is set.
 #pragma once
 
+#include <type_traits>
+
 #include "ptx.cuh"
 
 namespace mimo {
@@ -54,10 +56,6 @@ struct PrefillParams {
   // cover positions 0 .. nk-1; key rows at positions < krot_from are stored rotated.
   // Whole-sequence prefill: q_off = 0, nk = n, krot_from = 0.
   int q_off, nk, krot_from;
-  // first tokens that stay visible behind a window (kernels instantiated with FIRST only), and
-  // the V rows as the caller gave them
-  int n_first;
-  const __nv_bfloat16* v;  // [B, nk, Hkv, 128]
   unsigned* err;
   unsigned long long* trace;   // debug timestamps (builds with -DMIMO_TRACE only), else null
 };
@@ -69,6 +67,22 @@ __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
                  "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
                  "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
+// Of the kernels with first tokens that stay visible behind a window.
+struct PrefillFirstParams : PrefillParams {
+  int n_first;
+  const __nv_bfloat16* v;  // [B, nk, Hkv, 128], the rows as the caller gave them
+  double invf[96];         // theta^(-2k/rot), from the host (a double pow is the longest step of a kernel's start)
+};
+template <bool FIRST>
+using PrefillParamsOf = std::conditional_t<FIRST, PrefillFirstParams, PrefillParams>;
+__device__ __forceinline__ int first_of(const PrefillFirstParams& p) { return p.n_first; }
+__device__ __forceinline__ int first_of(const PrefillParams&) { return 0; }
+// theta^(-2k/rot) of rotation pair k.
+__device__ __forceinline__ double inv_freq(const PrefillFirstParams& p, int k) { return p.invf[k]; }
+__device__ __forceinline__ double inv_freq(const PrefillParams& p, int k) {
+  return pow(p.rope_theta, -2.0 * k / static_cast<double>(p.rot_dims));
 }
 
 template <int G, int BN, int NKS>
@@ -185,7 +199,7 @@ constexpr uint16_t kNan16 = 0x7fffu;      // a NaN in bf16 and in f16
 template <int G, int BN, int NKS, bool FIRST = false>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, const PrefillParams p) {
+                   const __grid_constant__ CUtensorMap tmV, const PrefillParamsOf<FIRST> p) {
   using C = PfCfg<G, BN, NKS>;
   static_assert(NKS == 1 || NKS == 2, "K stages");
   static_assert(!FIRST || NKS == 2, "more than one tile per row block");
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   if (warp >= 2) {
     const int half = p.rot_dims >> 1;
     for (int k = threadIdx.x - 64; k < half; k += 128)
-      s_invf[k] = pow(p.rope_theta, -2.0 * k / static_cast<double>(p.rot_dims));
+      s_invf[k] = inv_freq(p, k);
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmQ);
@@ -422,7 +436,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const uint32_t sc = trow + ((it & 1) ? C::S1_COL : 0);
         const int kt0 = tile_key(j, lo);
         const int khi = FIRST && j < nft ? lo - 1 : pos;   // last key this tile may contribute
-        auto key_ok = [&](int key) -> bool { return (key >= klo || (FIRST && key < p.n_first)) && key <= khi; };
+        auto key_ok = [&](int key) -> bool { return (key >= klo || (FIRST && key < first_of(p))) && key <= khi; };
 
         // pass 1: row max over the valid keys of this tile
         float mx = -INFINITY;

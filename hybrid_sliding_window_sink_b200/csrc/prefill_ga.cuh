@@ -162,7 +162,7 @@ __device__ __forceinline__ void rope_q_row(uint32_t base, int row, int pos, int 
 template <int G, bool WIN = false>
 __global__ void __launch_bounds__(kGaThreads, 1)
     prefill_ga_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const PrefillParams p) {
+                      const __grid_constant__ CUtensorMap tmV, const PrefillParamsOf<WIN> p) {
   using L = GaLayout<G>;
   constexpr int P = L::P;
   extern __shared__ uint8_t smem_raw[];
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kGaThreads, 1)
     tmem_relinquish();
   }
   if (warp >= 2 && warp < 6 && threadIdx.x - 64 < half)
-    s_invf[threadIdx.x - 64] = pow(p.rope_theta, -2.0 * (threadIdx.x - 64) / static_cast<double>(p.rot_dims));
+    s_invf[threadIdx.x - 64] = inv_freq(p, threadIdx.x - 64);
   // Q rows past the sequence end are never loaded: start them (and all of Q) at zero
   for (int i = threadIdx.x; i < 2 * L::Q_BLOCK / 16; i += kGaThreads)
     reinterpret_cast<uint4*>(smem + L::OFF_Q)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kGaThreads, 1)
   };
   // (WIN) whether some row of positions [plo, phi] masks a key of the tile at kt0
   auto partly = [&](int kt0, int plo, int phi) -> bool {
-    return kt0 + kGaBN - 1 > plo || (kt0 < phi - p.window + 1 && kt0 + kGaBN > p.n_first);
+    return kt0 + kGaBN - 1 > plo || (kt0 < phi - p.window + 1 && kt0 + kGaBN > first_of(p));
   };
 
   if (warp == 0) {
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kGaThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int k0 = kc + 32 * h;
-          const uint32_t valid = bits_below(pos + 1 - k0) & (~bits_below(pos - p.window + 1 - k0) | bits_below(p.n_first - k0));
+          const uint32_t valid = bits_below(pos + 1 - k0) & (~bits_below(pos - p.window + 1 - k0) | bits_below(first_of(p) - k0));
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[32 * h + e] = valid >> e & 1u ? v[32 * h + e] : 0xff800000u;
         }

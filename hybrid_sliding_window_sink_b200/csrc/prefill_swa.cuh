@@ -110,7 +110,8 @@ enum : int {
   kSwFirstFull = 50,  // (FIRST) the first tokens' unit: landed, rotated (128 arrivals), free again
   kSwFirstReady = 51,
   kSwFirstFree = 52,
-  kSwNumBars = 53
+  kSwTurn = 53,       // (FIRST) the turns of a run's start are in the spare table (128 arrivals)
+  kSwNumBars = 54
 };
 
 // (x, y) <- (x cos - y sin, y cos + x sin) for two rotation pairs: xw and yw each hold two
@@ -186,7 +187,7 @@ __device__ __forceinline__ void rope_row_tab(uint8_t* row_base, int row, int nun
 template <bool FIRST>
 __global__ void __launch_bounds__(kSwaThreads, 1)
     prefill_swa_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const PrefillParams p) {
+                       const __grid_constant__ CUtensorMap tmV, const PrefillParamsOf<FIRST> p) {
   using L = SwaLayout<FIRST>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
     for (int i = 0; i < kSwNumBars; ++i) {
       const bool many = (i >= kSwQReady && i < kSwQReady + 2) || (i >= kSwPReady && i < kSwPReady + 2) ||
                         (i >= kSwTmFree && i < kSwTab + 2) ||
-                        (i >= kSwKReady && i < kSwKReady + kSwaUnits) || i == kSwFirstReady;
+                        (i >= kSwKReady && i < kSwKReady + kSwaUnits) || i == kSwFirstReady || i == kSwTurn;
       mbar_init(bar(i), many ? 128u : 1u);
     }
     *s_abort = 0;
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
     tmem_relinquish();
   }
   if (warp >= 2 && warp < 6 && threadIdx.x - 64 < half)
-    s_invf[threadIdx.x - 64] = pow(p.rope_theta, -2.0 * (threadIdx.x - 64) / static_cast<double>(p.rot_dims));
+    s_invf[threadIdx.x - 64] = inv_freq(p, threadIdx.x - 64);
   // the ring starts zeroed: slots outside a window are read (masked) before they are filled
   for (int o = threadIdx.x * 16; o < 3 * L::R_CHUNK + 2 * L::R_CHUNK; o += kSwaThreads * 16)
     *reinterpret_cast<uint4*>(smem + L::OFF_K + o) = make_uint4(0u, 0u, 0u, 0u);
@@ -515,7 +516,56 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         if (first) {                                 // and the first tokens' unit of a new run
           if (!wait_all(bar(kSwFirstFull), runs & 1)) break;
           v_unit(kSwaUnits);
-          if (half > 0 && ctid < 16) {
+          if (half == 32) {
+            // K of the window's units and of the first tokens, two units per turn: thread (row, 16-byte
+            // unit) takes the angles of its unit's first position from the lanes (frequency = lane) and
+            // turns them by its row's. The turns j w_k (see `turn`) are handed around in the table that
+            // the next block will write (its last reader was the previous block).
+            float* spare = reinterpret_cast<float*>(smem + L::OFF_TAB + ((i + 1) & 1) * L::TAB_BYTES);
+#pragma unroll
+            for (int i2 = 0; i2 < 4; ++i2) {
+              float* tk = spare + ((ctid >> 5) + 4 * i2) * 64 + (lane >> 1) * 4 + (lane & 1);
+              tk[0] = turn[i2].x;
+              tk[2] = turn[i2].y;
+            }
+            mbar_arrive(bar(kSwTurn));
+            if (!wait_all(bar(kSwTurn), runs & 1)) break;
+            const int row = (ctid >> 2) & 15, u = ctid & 3;
+            const float4* t4 = reinterpret_cast<const float4*>(spare + row * 64);
+#pragma unroll 1
+            for (int k2 = ctid >> 6; k2 <= kSwaWin; k2 += 2) {   // 0 .. 8: the window's, 9: the first tokens'
+              const bool own = k2 < kSwaWin;
+              const int kpos0 = own ? p0 - 128 + 16 * k2 : 0, kpos = kpos0 + row;
+              const int ring_row = (own ? (s_first + k2) % kSwaUnits : kSwaUnits) * 16 + row;
+              const double ang = static_cast<double>(kpos0) * s_invf[lane];
+              const double nrev = rint(ang * 0.15915494309189535);
+              float bs, bc;
+              __sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &bs, &bc);
+              const bool raw = kpos >= p.krot_from && kpos < p.nk, cooked = kpos >= 0 && kpos < p.krot_from;
+              uint4* px = reinterpret_cast<uint4*>(smem + L::OFF_K + ring_row * 128 + ((u ^ (row & 7)) << 4));
+              uint4* py = reinterpret_cast<uint4*>(smem + L::OFF_K + ring_row * 128 + (((u + 4) ^ (row & 7)) << 4));
+              const uint4 x = *px, y = *py;
+              uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int e2 = 0; e2 < 4; ++e2) {
+                const int k = u * 8 + 2 * e2;
+                const float4 t = t4[u * 4 + e2];
+                const float c0 = __shfl_sync(0xffffffffu, bc, k), s0 = __shfl_sync(0xffffffffu, bs, k);
+                const float c1 = __shfl_sync(0xffffffffu, bc, k + 1), s1 = __shfl_sync(0xffffffffu, bs, k + 1);
+                if (raw) {
+                  rot_pair(xs[e2], ys[e2], make_float4(c0 * t.x - s0 * t.z, c1 * t.y - s1 * t.w,
+                                                       s0 * t.x + c0 * t.z, s1 * t.y + c1 * t.w));
+                } else if (cooked) {
+                  xs[e2] = bf16x2_to_f16x2(xs[e2]);
+                  ys[e2] = bf16x2_to_f16x2(ys[e2]);
+                }
+              }
+              if (raw || cooked) {
+                *px = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+                *py = make_uint4(ys[0], ys[1], ys[2], ys[3]);
+              }
+            }
+          } else if (half > 0 && ctid < 16) {
             const int ring_row = kSwaUnits * 16 + ctid;
             if (ctid >= p.krot_from && ctid < p.nk) rope_row(sK, L::R_CHUNK, ring_row, ctid, p.rot_dims, s_invf);
             else if (ctid < p.krot_from) f16_row(sK, L::R_CHUNK, ring_row, p.rot_dims);
@@ -526,7 +576,9 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         }
       }
       if (half > 0) {
-        if (first) {
+        if (FIRST && first && half == 32) {
+          // done above
+        } else if (first) {
           for (int rr = ctid; rr < 16 * kSwaWin; rr += 128) {
             const int kpos = p0 - 128 + rr;
             const int ring_row = ((s_first + rr / 16) % kSwaUnits) * 16 + (rr & 15);
@@ -585,8 +637,9 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       auto block_class = [&](int c, int& elo, int& ehi) -> int {
         if (FIRST && c == kSwaUnits) {   // first tokens below this row's window
           elo = 0;
-          ehi = min(p.n_first, klo) - 1;
-          return min(p.n_first, klo_max) <= 0 ? 0 : (min(p.n_first, klo_min) >= 16 ? 2 : 1);
+          const int nfirst = first_of(p);
+          ehi = min(nfirst, klo) - 1;
+          return min(nfirst, klo_max) <= 0 ? 0 : (min(nfirst, klo_min) >= 16 ? 2 : 1);
         }
         int d = um - c;
         d += d < 0 ? kSwaUnits : 0;
