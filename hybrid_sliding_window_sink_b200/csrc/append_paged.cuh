@@ -31,6 +31,8 @@ struct AppendPagedParams {
   const int* n_new;           // [B] tokens to write (null: n)
   int page_stride;
   int B, n, Hkv, rot, page_size, max_pages, num_pages, tokens;   // tokens: per CTA
+  uint32_t div_mul;           // t / page_size = (t * div_mul) >> div_shift for t < 2^31
+  int div_shift;
   double invf[kDQK / 2];      // theta^(-2d/rot)
 };
 
@@ -55,13 +57,23 @@ __device__ __forceinline__ uint32_t amax8(const float (&f)[8]) {
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
   return m;
 }
-// f / sc of a row. The reciprocal's rounding (2^-23) is far below e4m3's half step (2^-4); scales
-// whose reciprocal leaves fp32's range are divided by.
-__device__ __forceinline__ void scale8(float (&f)[8], float sc) {
-  if (sc >= 7.52e-37f) {                      // 2^-120
-    const float r = 1.f / sc;
+// The scale amax / 448 of a row (1 for zeros) and its reciprocal. Multiplications: the scale is off
+// by one rounding (2^-24) and x / scale by 2^-22, far below e4m3's half step (2^-4). Magnitudes
+// whose reciprocal may leave fp32's range take the divisions.
+__device__ __forceinline__ float row_scale(uint32_t amax_bits, float& inv) {
+  const float a = __uint_as_float(amax_bits);
+  if (a > 1e-30f && a < 1e30f) {
+    inv = __fdividef(448.f, a);
+    return a * (1.f / 448.f);
+  }
+  const float sc = a / 448.f;
+  inv = 0.f;                                  // x / scale by division
+  return sc == 0.f ? 1.f : sc;
+}
+__device__ __forceinline__ void scale8(float (&f)[8], float sc, float inv) {
+  if (inv != 0.f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] *= r;
+    for (int i = 0; i < 8; ++i) f[i] *= inv;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] /= sc;
@@ -109,7 +121,7 @@ __global__ void __launch_bounds__(kApThreads) append_paged_kernel(const __grid_c
       const long long pos = pos0 + t;
       put[k] = put[k] && pos >= 0 && pos < most;     // outside the table: not written
       if (put[k]) {
-        const int pg = static_cast<int>(static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page_size));
+        const int pg = static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.div_mul) >> p.div_shift);
         const int ent = __ldg(p.table + static_cast<long long>(b) * p.max_pages + pg);
         const long long src = (static_cast<long long>(b) * p.n + i0) * p.Hkv + r;
         if (is_k) {
@@ -148,22 +160,21 @@ __global__ void __launch_bounds__(kApThreads) append_paged_kernel(const __grid_c
       if constexpr (FP8) {
         unpack8(x1[k], h);                           // V: second unit (zeros on K lanes)
         const uint32_t top = max(amax8(f), amax8(h));
-        float sk = __uint_as_float(__reduce_max_sync(0xffffffffu, is_k ? top : 0u)) / 448.f;
-        float sv = __uint_as_float(__reduce_max_sync(0xffffffffu, is_k ? 0u : top)) / 448.f;
-        sk = sk == 0.f ? 1.f : sk;
-        sv = sv == 0.f ? 1.f : sv;
-        const float sc = is_k ? sk : sv;
-        scale8(f, sc);
+        const uint32_t ak = __reduce_max_sync(0xffffffffu, is_k ? top : 0u);
+        const uint32_t av = __reduce_max_sync(0xffffffffu, is_k ? 0u : top);
+        float inv;
+        const float sc = row_scale(is_k ? ak : av, inv);
+        scale8(f, sc, inv);
         const uint2 lo = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
         if (is_k) {
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kc) + d * kDQK + lane * 8) = lo;
         } else {
-          scale8(h, sc);
+          scale8(h, sc, inv);
           *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.vc) + d * kDV + (lane - 24) * 16) =
               make_uint4(lo.x, lo.y, e4m3x4(h[0], h[1], h[2], h[3]), e4m3x4(h[4], h[5], h[6], h[7]));
         }
-        if (lane == 0) p.ks[d] = sk;
-        if (lane == 24) p.vs[d] = sv;
+        if (lane == 0) p.ks[d] = sc;
+        if (lane == 24) p.vs[d] = sc;
       } else {
         if (is_k) {
           if (lane < 2 * nun)

@@ -769,6 +769,15 @@ mimo_status check_pages(const mimo_pages* pg, int hkv) {
   return MIMO_OK;
 }
 
+// t / d = (t * mul) >> shift for t < 2^31: shift = 31 + l with l = ceil(log2 d), mul = ceil(2^shift / d).
+// mul d exceeds 2^shift by less than d <= 2^l, so t's share of it stays below one step.
+void page_divisor(int d, uint32_t& mul, int& shift) {
+  int l = 0;
+  while ((1LL << l) < d) ++l;
+  shift = 31 + l;
+  mul = static_cast<uint32_t>(((1ULL << shift) + d - 1) / d);
+}
+
 // CTAs of the paged decode (all resident at once) and its workspace: headers of the
 // units that a run boundary cuts, then two slots of G rows per CTA.
 struct PagedPlan {
@@ -882,12 +891,7 @@ mimo_status run_paged(const mimo_shape* s, const void* q, const void* k, const v
   prm.window = window;
   prm.n_first = n_first;
   prm.nctas = pl.nctas;
-  // t / d = (t * m) >> (31 + l) for t < 2^31, with l = ceil(log2 d) and m = ceil(2^(31 + l) / d):
-  // m d exceeds 2^(31 + l) by less than d <= 2^l, so t's share of it stays below one step
-  int l = 0;
-  while ((1LL << l) < pg->page_size) ++l;
-  prm.div_shift = 31 + l;
-  prm.div_mul = static_cast<uint32_t>(((1ULL << (31 + l)) + pg->page_size - 1) / pg->page_size);
+  page_divisor(pg->page_size, prm.div_mul, prm.div_shift);
   prm.scale_log2 = scale_log2_of(s);
 #ifdef MIMO_DEBUG   // the only reports of these kernels are the debug builds' (no wait can give up)
   prm.err = device_error_ptr(dev);
@@ -944,6 +948,7 @@ mimo_status run_append_paged(const mimo_shape* s, const void* k_new, const void*
   prm.page_size = pg->page_size;
   prm.max_pages = pg->max_pages;
   prm.num_pages = pg->num_pages;
+  page_divisor(pg->page_size, prm.div_mul, prm.div_shift);
   for (int d = 0; d < rot / 2; ++d) prm.invf[d] = std::pow(static_cast<double>(theta), -2.0 * d / rot);
   const size_t smem = static_cast<size_t>(prm.tokens) * (rot / 2) * sizeof(float2);   // <= 24 KB
   mimo::append_paged_kernel<FP8><<<static_cast<unsigned>(blocks), mimo::kApThreads, smem, static_cast<cudaStream_t>(stream)>>>(prm);
