@@ -519,6 +519,8 @@ def prefill_first(q, k, v, sink=None, *, window, n_first, pos_offset=0, k_prefix
                                  softmax_scale, want_lse)
         if got is not None:
             return got
+    window, n_first, pos_offset, rot_dims = int(window), int(n_first), int(pos_offset), int(rot_dims)
+    rope_theta, softmax_scale = float(rope_theta), float(softmax_scale)
     dev = _cuda_device(q, "q")
     _need_at(q, "q", torch.bfloat16, (None, None, None, 192), dev)
     B, n, hq, _ = q.shape
@@ -615,6 +617,7 @@ def _decode_paged(q, k, v, scales, table, lengths, sink, window, n_first, softma
         got = call.decode_paged(q, k, v, ks, vs, table, lengths, sink, window, n_first, softmax_scale, want_lse)
         if got is not None:
             return got
+    window, n_first, softmax_scale = int(window), int(n_first), float(softmax_scale)
     dev = _cuda_device(q, "q")
     _need_at(q, "q", torch.bfloat16, (None, None, 192), dev)
     B, hq, _ = q.shape
@@ -675,7 +678,8 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, lengths
 
 def decode_paged_workspace_size(batch, hq, hkv, *, max_pages, page_size, window=0, n_first=0):
     """Bytes of workspace the paged decodes need on the current device."""
-    return _paged_workspace(torch.cuda.current_device(), batch, hq, hkv, max_pages, page_size, window, n_first)
+    return _paged_workspace(torch.cuda.current_device(), int(batch), int(hq), int(hkv), int(max_pages), int(page_size),
+                            int(window), int(n_first))
 
 
 def _append_paged(k_new, v_new, k, v, scales, table, positions, n_new, rope_theta, rot_dims, stream):
@@ -683,6 +687,7 @@ def _append_paged(k_new, v_new, k, v, scales, table, positions, n_new, rope_thet
         ks, vs = (None, None) if scales is None else scales
         if call.append_paged(k_new, v_new, k, v, ks, vs, table, positions, n_new, rope_theta, rot_dims):
             return
+    rope_theta, rot_dims = float(rope_theta), int(rot_dims)
     dev = _cuda_device(k_new, "k_new")
     _need_at(k_new, "k_new", torch.bfloat16, (None, None, None, 192), dev)
     B, n, hkv, _ = k_new.shape

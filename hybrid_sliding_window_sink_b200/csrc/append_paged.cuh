@@ -7,9 +7,13 @@
 //
 // The bytes bound it (640 read and 640, or 328, written per row). A CTA takes kApTokens tokens
 // of one sequence with all their heads: the (cos, sin) of a token is computed once for its heads
-// (the frequencies theta^(-2d/rot) come from the host), and a warp writes one row at a time:
-// lanes 0-23 the 16-byte units of K (a unit's partner comes from its lane by a shuffle), lanes
-// 24-31 two units of V each, so a row's amax is a warp reduction.
+// (the frequencies theta^(-2d/rot) come from the host), and half a warp writes a row: lane l its V
+// unit l (16 bytes) and, for l < 12, two K units, the partners u and u + rot/16 of the rotation where
+// it rotates. So no value crosses lanes but the row's two maxima, and the row's index arithmetic is
+// shared by two rows of a warp; the first rows' loads are under way while the angles are worked
+// out. 8192 tokens x 4 heads into FP8 pages (31.7 MB, 4.9 us at the copy rate): a row per warp with
+// partners by shuffles 16.6 us, this 12.4 (64 registers: four CTAs per SM; three 13.4, five spill, 13.7).
+// What is left is a CTA's chain of waits (position, table entry, angles) over two waves of CTAs.
 #pragma once
 
 #include "ptx.cuh"
@@ -81,7 +85,7 @@ __device__ __forceinline__ void scale8(float (&f)[8], float sc, float inv) {
 }
 
 template <bool FP8>
-__global__ void __launch_bounds__(kApThreads) append_paged_kernel(const __grid_constant__ AppendPagedParams p) {
+__global__ void __launch_bounds__(kApThreads, 4) append_paged_kernel(const __grid_constant__ AppendPagedParams p) {
   extern __shared__ float2 s_cs[];            // [tokens][rot / 2] (cos, sin)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tiles = (p.n - 1) / p.tokens + 1;
@@ -92,6 +96,103 @@ __global__ void __launch_bounds__(kApThreads) append_paged_kernel(const __grid_c
   if (count <= 0) return;
   const long long pos0 = static_cast<long long>(__ldg(p.pos + b)) + i0;
   const long long most = static_cast<long long>(p.max_pages) * p.page_size;
+  // two rows per half warp at a time, so that their loads are in flight together
+  const int rows = count * p.Hkv;
+  const int l = lane & 15, sub = lane >> 4;
+  const bool has_k = l < 12, turned = l < nun;
+  const int u0 = turned ? l : 2 * l, u1 = turned ? l + nun : 2 * l + 1;
+  constexpr int kStep = 2 * (kApThreads / 32);       // rows that all warps take in one go
+  uint32_t dst[2];
+  int tok[2];
+  bool put[2];
+  uint4 a[2], b2[2], c[2];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = r0 + k * kStep;
+      put[k] = r < rows;
+      dst[k] = 0;
+      a[k] = b2[k] = c[k] = make_uint4(0u, 0u, 0u, 0u);
+      const int t = r / p.Hkv, g = r - t * p.Hkv;
+      tok[k] = put[k] ? t : 0;
+      const long long pos = pos0 + t;
+      put[k] = put[k] && pos >= 0 && pos < most;     // outside the table: not written
+      if (put[k]) {
+        const int pg = static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.div_mul) >> p.div_shift);
+        const int ent = __ldg(p.table + static_cast<long long>(b) * p.max_pages + pg);
+        const long long src = (static_cast<long long>(b) * p.n + i0) * p.Hkv + r;
+        if (has_k) {
+          a[k] = *reinterpret_cast<const uint4*>(p.k + src * kDQK + u0 * 8);
+          b2[k] = *reinterpret_cast<const uint4*>(p.k + src * kDQK + u1 * 8);
+        }
+        c[k] = *reinterpret_cast<const uint4*>(p.v + src * kDV + l * 8);
+        put[k] = static_cast<unsigned>(ent) < static_cast<unsigned>(p.num_pages);
+        // (token, KV head) rows of a pool number less than 2^31 (checked by the host)
+        if (put[k]) dst[k] = static_cast<uint32_t>((ent * p.page_stride + static_cast<int>(pos) - pg * p.page_size) * p.Hkv + g);
+      }
+    }
+  };
+  auto work = [&]() {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float f[8], h[8];
+      unpack8(a[k], f);
+      unpack8(b2[k], h);
+      if (turned) {
+        const float2* cs = s_cs + tok[k] * half + l * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 w = cs[i];
+          const float x = f[i], y = h[i];
+          f[i] = x * w.x - y * w.y;
+          h[i] = y * w.x + x * w.y;
+        }
+      }
+      const uint64_t d = dst[k];
+      if constexpr (FP8) {
+        float v[8];
+        unpack8(c[k], v);
+        uint32_t ak = max(amax8(f), amax8(h)), av = amax8(v);   // zeros on lanes without K
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+          ak = max(ak, __shfl_xor_sync(0xffffffffu, ak, o));
+          av = max(av, __shfl_xor_sync(0xffffffffu, av, o));
+        }
+        float ik, iv;
+        const float sk = row_scale(ak, ik), sv = row_scale(av, iv);
+        scale8(f, sk, ik);
+        scale8(h, sk, ik);
+        scale8(v, sv, iv);
+        if (put[k]) {
+          uint8_t* kc = static_cast<uint8_t*>(p.kc) + d * kDQK;
+          if (has_k) {
+            *reinterpret_cast<uint2*>(kc + u0 * 8) = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+            *reinterpret_cast<uint2*>(kc + u1 * 8) = make_uint2(e4m3x4(h[0], h[1], h[2], h[3]), e4m3x4(h[4], h[5], h[6], h[7]));
+          }
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.vc) + d * kDV + l * 8) =
+              make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+          if (l == 0) {
+            p.ks[d] = sk;
+            p.vs[d] = sv;
+          }
+        }
+      } else if (put[k]) {
+        __nv_bfloat16* kc = static_cast<__nv_bfloat16*>(p.kc) + d * kDQK;
+        if (turned) {
+          a[k] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+          b2[k] = make_uint4(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]), pack_bf16(h[4], h[5]), pack_bf16(h[6], h[7]));
+        }
+        if (has_k) {
+          *reinterpret_cast<uint4*>(kc + u0 * 8) = a[k];
+          *reinterpret_cast<uint4*>(kc + u1 * 8) = b2[k];
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.vc) + d * kDV + l * 8) = c[k];
+      }
+    }
+  };
+  int r0 = 2 * warp + sub;
+  bool more = r0 - sub < rows;                       // the same for the whole warp
+  if (more) load(r0);                                // under way while the angles are worked out
   for (int x = tid; x < count * half; x += kApThreads) {
     const int t = x / half, d = x - t * half;
     const double ang = static_cast<double>(pos0 + t) * p.invf[d];
@@ -101,92 +202,11 @@ __global__ void __launch_bounds__(kApThreads) append_paged_kernel(const __grid_c
     s_cs[x] = make_float2(cs, sn);
   }
   __syncthreads();
-  // two rows of the warp at a time, so that both rows' loads are in flight together
-  const int rows = count * p.Hkv;
-  const bool is_k = lane < 24;
-  const int peer = lane < nun ? lane + nun : (lane < 2 * nun ? lane - nun : lane);
-  for (int r0 = warp; r0 < rows; r0 += 2 * (kApThreads / 32)) {
-    uint32_t dst[2];
-    int tok[2];
-    bool put[2];
-    uint4 x0[2], x1[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = r0 + k * (kApThreads / 32);
-      put[k] = r < rows;
-      dst[k] = 0;
-      x0[k] = x1[k] = make_uint4(0u, 0u, 0u, 0u);
-      const int t = r / p.Hkv, g = r - t * p.Hkv;
-      tok[k] = put[k] ? t : 0;
-      const long long pos = pos0 + t;
-      put[k] = put[k] && pos >= 0 && pos < most;     // outside the table: not written
-      if (put[k]) {
-        const int pg = static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.div_mul) >> p.div_shift);
-        const int ent = __ldg(p.table + static_cast<long long>(b) * p.max_pages + pg);
-        const long long src = (static_cast<long long>(b) * p.n + i0) * p.Hkv + r;
-        if (is_k) {
-          x0[k] = *reinterpret_cast<const uint4*>(p.k + src * kDQK + lane * 8);
-        } else {
-          const uint4* pv = reinterpret_cast<const uint4*>(p.v + src * kDV + (lane - 24) * 16);
-          x0[k] = pv[0];
-          x1[k] = pv[1];
-        }
-        put[k] = static_cast<unsigned>(ent) < static_cast<unsigned>(p.num_pages);
-        // (token, KV head) rows of a pool number less than 2^31 (checked by the host)
-        if (put[k]) dst[k] = static_cast<uint32_t>((ent * p.page_stride + static_cast<int>(pos) - pg * p.page_size) * p.Hkv + g);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      // the partner unit of the rotation, lane + nun or lane - nun
-      uint4 y;
-      y.x = __shfl_sync(0xffffffffu, x0[k].x, peer);
-      y.y = __shfl_sync(0xffffffffu, x0[k].y, peer);
-      y.z = __shfl_sync(0xffffffffu, x0[k].z, peer);
-      y.w = __shfl_sync(0xffffffffu, x0[k].w, peer);
-      if (!put[k]) continue;                         // the same for the whole warp
-      float f[8], h[8];
-      unpack8(x0[k], f);
-      if (lane < 2 * nun) {
-        unpack8(y, h);
-        const float2* cs = s_cs + tok[k] * half + (lane < nun ? lane : lane - nun) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 w = cs[i];
-          f[i] = lane < nun ? f[i] * w.x - h[i] * w.y : f[i] * w.x + h[i] * w.y;
-        }
-      }
-      const uint64_t d = dst[k];
-      if constexpr (FP8) {
-        unpack8(x1[k], h);                           // V: second unit (zeros on K lanes)
-        const uint32_t top = max(amax8(f), amax8(h));
-        const uint32_t ak = __reduce_max_sync(0xffffffffu, is_k ? top : 0u);
-        const uint32_t av = __reduce_max_sync(0xffffffffu, is_k ? 0u : top);
-        float inv;
-        const float sc = row_scale(is_k ? ak : av, inv);
-        scale8(f, sc, inv);
-        const uint2 lo = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
-        if (is_k) {
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kc) + d * kDQK + lane * 8) = lo;
-        } else {
-          scale8(h, sc, inv);
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.vc) + d * kDV + (lane - 24) * 16) =
-              make_uint4(lo.x, lo.y, e4m3x4(h[0], h[1], h[2], h[3]), e4m3x4(h[4], h[5], h[6], h[7]));
-        }
-        if (lane == 0) p.ks[d] = sc;
-        if (lane == 24) p.vs[d] = sc;
-      } else {
-        if (is_k) {
-          if (lane < 2 * nun)
-            x0[k] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.kc) + d * kDQK + lane * 8) = x0[k];
-        } else {
-          uint4* pv = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.vc) + d * kDV + (lane - 24) * 16);
-          pv[0] = x0[k];
-          pv[1] = x1[k];
-        }
-      }
-    }
+  while (more) {
+    work();
+    r0 += 2 * kStep;
+    more = r0 - sub < rows;
+    if (more) load(r0);
   }
 }
 

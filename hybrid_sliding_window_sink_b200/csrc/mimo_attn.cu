@@ -1301,7 +1301,7 @@ mimo_status mimo_attn_verify_drafts(int batch, int n_drafts, int vocab, int prob
   if (!target_probs || !uniforms || !n_accepted || !tokens || (n_drafts > 0 && !draft_tokens)) return MIMO_ERR_NULL;
   if (batch < 1 || n_drafts < 0 || vocab < 1) return MIMO_ERR_SHAPE;
   if (probs_type != MIMO_PROBS_F32 && probs_type != MIMO_PROBS_BF16) return MIMO_ERR_SHAPE;
-  if (batch > 65535 || n_drafts == 0x7fffffff) return MIMO_ERR_UNSUPPORTED;
+  if (batch > 65535 || n_drafts == 0x7fffffff || vocab > (1 << 30)) return MIMO_ERR_UNSUPPORTED;   // 32-bit places in a row
   const uintptr_t pa = probs_type == MIMO_PROBS_F32 ? 4 : 2;
   if (!aligned(target_probs, pa) || (draft_probs && !aligned(draft_probs, pa)) ||
       (draft_tokens && !aligned(draft_tokens, 4)) || !aligned(uniforms, 4) || (n_valid && !aligned(n_valid, 4)) ||
@@ -1427,7 +1427,7 @@ const char* mimo_status_string(mimo_status st) {
   return "unknown status";
 }
 
-int mimo_attn_version(void) { return 100; }
+int mimo_attn_version(void) { return 200; }
 
 #ifdef MIMO_TEST_HOOKS
 int mimo_attn_test_stuck_wait(void* stream) {

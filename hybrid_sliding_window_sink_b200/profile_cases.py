@@ -19,6 +19,14 @@ Cases:
                         64 Q / 4 KV heads (row-block pair kernel)
   chunk_swa_c8192_p8192 SWA chunked prefill: 8192-token chunk after an 8192-token rotated prefix,
                         64 Q / 8 KV heads, W=128 (K/V-ring kernel)
+  paged_b64_ragged      paged decode, B=64, 1024-16384 tokens in pages of 64, 64 Q / 4 KV heads
+  paged_fp8_b2_long     paged decode over FP8 pages of 128, B=2, 100k-131k tokens, 64 Q / 4 KV heads
+  append_fp8_n4096      page writes, B=2, 4096 tokens, 4 KV heads, FP8 pages of 64
+  first_swa_n8192       window prefill with 4 pinned first tokens, n=8192, 64 Q / 8 KV heads, W=128
+                        (K/V-ring kernel)
+  first_wide_n8192      window prefill with 64 pinned first tokens, n=8192, 64 Q / 4 KV heads, W=2048
+                        (row-block pair kernel)
+  verify_b64_v131072    draft verification, B=64, 3 drafts, 131072 tokens, fp32
   select_b8_l65536      token selection, B=8, L=65536, 64 Q / 4 KV heads, the 1024 best
                         outside the recent 128
 Prints the mean time per call over --reps calls (after two warm-up calls).
@@ -36,7 +44,45 @@ from . import _lib
 from . import workloads as wl
 
 
+def _paged(lengths, hkv, page, fp8, dev):
+    """Pools, a random block table, lengths, q and sink of a paged decode case."""
+    g = wl._gen(13, dev)
+    B, width = len(lengths), -(-max(lengths) // page)
+    table = torch.randperm(B * width, generator=g, device=dev).view(B, width).int()
+    if fp8:
+        k, v, ks, vs = wl.random_fp8_cache(B * width, page, hkv, seed=14, device=dev)
+        pools = (k, v, ks, vs)
+    else:
+        pools = tuple(wl._randn_bf16((B * width, page, hkv, d), g, dev) for d in (wl.DQK, wl.DV))
+    q = wl._randn_bf16((B, 64, wl.DQK), g, dev)
+    return q, pools, table, torch.tensor(lengths, dtype=torch.int32, device=dev), torch.randn(64, generator=g, device=dev)
+
+
 def _case(name, dev):
+    if name == "paged_b64_ragged":
+        L = wl.lengths_uniform(64, 1024, 16384, seed=13).tolist()
+        q, pools, table, lengths, sink = _paged(L, 4, 64, False, dev)
+        return lambda: _lib.decode_paged(q, *pools, table, lengths, sink)
+    if name == "paged_fp8_b2_long":
+        q, pools, table, lengths, sink = _paged([131072, 100001], 4, 128, True, dev)
+        return lambda: _lib.decode_paged_fp8(q, *pools, table, lengths, sink)
+    if name == "append_fp8_n4096":
+        _, pools, table, _, _ = _paged([4096, 4096], 4, 64, True, dev)
+        g = wl._gen(15, dev)
+        kn, vn = (wl._randn_bf16((2, 4096, 4, d), g, dev) for d in (wl.DQK, wl.DV))
+        pos = torch.zeros(2, dtype=torch.int32, device=dev)
+        return lambda: _lib.cache_append_paged_fp8(kn, vn, *pools, table, pos)
+    if name in ("first_swa_n8192", "first_wide_n8192"):
+        hkv, W, F, theta = (8, 128, 4, 1e4) if name == "first_swa_n8192" else (4, 2048, 64, 1e7)
+        inp = wl.prefill_inputs(1, 8192, 64, hkv, seed=1, device=dev)
+        return lambda: _lib.prefill_first(inp["q"], inp["k"], inp["v"], inp["sink"], window=W, n_first=F, rope_theta=theta)
+    if name == "verify_b64_v131072":
+        g = wl._gen(16, dev)
+        p = torch.softmax(torch.randn(64, 4, 131072, generator=g, device=dev) * 3, -1)
+        qd = torch.softmax(torch.randn(64, 3, 131072, generator=g, device=dev) * 3, -1)
+        draft = torch.randint(0, 131072, (64, 3), generator=g, device=dev).int()
+        u = torch.rand(64, 4, generator=g, device=dev)
+        return lambda: _lib.verify_drafts(p, draft, u, qd)
     if name == "swa_prefill_n8192":
         inp = wl.prefill_inputs(1, 8192, 64, 8, seed=1, device=dev)
         return lambda: _lib.prefill(inp["q"], inp["k"], inp["v"], inp["sink"], window=128,

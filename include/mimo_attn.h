@@ -39,6 +39,8 @@
  *    to f16 without clamping (a larger |q| becomes infinite). A build compiled with
  *    MIMO_DEBUG records every such value in the device error word (bit 16, see
  *    mimo_attn_last_device_error). Outputs are rounded to bf16, lse is fp32.
+ *  - The paged decode carries P with 16 significant bits on bf16 pages and 11 on FP8 pages; its FP8
+ *    form multiplies Q in f16 as the FP8 decode does.
  *  - Thread safety: calls may be made from several host threads; the shared mutable
  *    state is the device error word read by mimo_attn_last_device_error and the scratch
  *    array of mimo_attn_sparse_noalloc (see there).
@@ -311,6 +313,9 @@ size_t mimo_attn_select_workspace_size(const mimo_shape* shape, int cache_capaci
  * pos_offset + n is mimo_attn_prefill_chunk itself. Positions stay absolute: a first token keeps
  * its own rotation. Errors as mimo_attn_prefill_chunk, MIMO_ERR_SHAPE also for n_first < 0.
  * The decode of such a layer is mimo_attn_decode_paged with the same window and n_first.
+ * A V row that is not finite does not reach queries that mask its key (behind them in a padded
+ * batch, say); queries that see a NaN in a V row become NaN, all 128 columns where the key's tile is
+ * masked in part.
  */
 mimo_status mimo_attn_prefill_first(const mimo_shape* shape, const void* q, const void* k, const void* v,
                                     int pos_offset, int k_prefix_rotated, const float* sink, int window,
@@ -411,11 +416,12 @@ enum { MIMO_PROBS_F32 = 0, MIMO_PROBS_BF16 = 1 };
  *   accepted a = the first t < n for which u[t] * q_t(x_t) < p_t(x_t) does not hold, or n;
  *   w(v) = max(p_a(v) - q_a(v), 0) if a < n, p_n(v) if a = n;
  *   next token = the smallest v with w(0) + .. + w(v) > u[T] * (sum of w).
- * The rows need not sum to 1. Negative and non-finite weights count as 0. Where nothing is left
- * of p_a - q_a, p_a itself is sampled; a target row without mass gives the token -1.
+ * The rows need not sum to 1 (but to less than 2^127). Negative and non-finite weights count as 0.
+ * Where nothing is left of p_a - q_a, p_a itself is sampled; a target row without mass gives the
+ * token -1. u q < p is decided exactly; running sums are good to about 2^-43 of the total.
  *
  *  target_probs [B, T + 1, V] device; row t is the target's distribution of the token after t
- *               accepted drafts. fp32 or bf16 (probs_type); sums are taken in double
+ *               accepted drafts. fp32 or bf16 (probs_type); V <= 2^30
  *  draft_probs  [B, T, V] device, same type, or NULL: drafts chosen by argmax (q one-hot at x_t)
  *  draft_tokens [B, T] int32 device (NULL allowed when T = 0); a token outside [0, V) is rejected
  *  uniforms     [B, T + 1] fp32 device, in [0, 1); the last one draws the next token
@@ -424,8 +430,8 @@ enum { MIMO_PROBS_F32 = 0, MIMO_PROBS_BF16 = 1 };
  *  tokens       [B, T + 1] int32 device (written): the accepted drafts, the next token, then -1
  *
  * Errors: MIMO_ERR_NULL, MIMO_ERR_SHAPE (batch or vocab < 1, n_drafts < 0, an unknown type),
- * MIMO_ERR_UNSUPPORTED (batch > 65535), MIMO_ERR_ALIGN (a pointer not aligned to its type; no
- * 16-byte rule here), MIMO_ERR_CUDA. No workspace.
+ * MIMO_ERR_UNSUPPORTED (batch > 65535, vocab > 2^30), MIMO_ERR_ALIGN (a pointer not aligned to its
+ * type; no 16-byte rule here), MIMO_ERR_CUDA. No workspace.
  */
 mimo_status mimo_attn_verify_drafts(int batch, int n_drafts, int vocab, int probs_type,
                                     const void* target_probs, const void* draft_probs,

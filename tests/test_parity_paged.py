@@ -3,8 +3,6 @@
 Bounds (serve_util.check): P has 16 significant bits on bf16 pages (two bf16 terms: 2^-16 with the
 remainder's own rounding) and 11 on FP8 pages (f16 half step 2^-11)."""
 
-import ctypes
-
 import numpy as np
 import pytest
 import torch
@@ -441,8 +439,11 @@ def test_the_two_marshallings_agree(cuda_device):
             _lib.decode_paged(*a, window=64, n_first=3)
     with pytest.raises(_lib.MimoError, match="SHAPE"):
         _lib.decode_paged(*args, n_first=-1)
-    with pytest.raises((TypeError, ctypes.ArgumentError)):
+    with pytest.raises((TypeError, ValueError)):
         _lib.decode_paged(*args, window="no")
+    wide = _lib.decode_paged(*args, window=np.int64(64), n_first=np.int32(3), softmax_scale=0)
+    torch.cuda.synchronize()
+    assert torch.equal(wide[0], out)
     with pytest.raises(TypeError):
         lib._usual().decode_paged(1)
 

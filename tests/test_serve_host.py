@@ -101,7 +101,7 @@ def test_verify_rejects(L):
         assert call(**{name: ODD}) == 4, name
     assert call(kind=1, p=P(0x10001)) == 4 and call(kind=1, q=P(0x10001)) == 4
     assert call(B=0) == 2 and call(T=-1) == 2 and call(V=0) == 2 and call(kind=2) == 2
-    assert call(B=65536) == 3
+    assert call(B=65536) == 3 and call(V=2 ** 30 + 1) == 3
 
 
 def test_python_side_rejects_cpu_tensors():
