@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
     before = __shfl_sync(0xffffffffu, before, l);
     if (found / kVfWarps == rank) {         // (the same for the whole CTA)
       // this CTA holds the piece: four consecutive tokens a thread, and so on until the running
-      // sum passes the target (at the first round for a row of up to 2^17 tokens)
+      // sum passes the target (at the first round for a row of up to 2^16 tokens)
       const int w0 = found * prm.piece;
       const int end = static_cast<int>(min(static_cast<long long>(w0) + prm.piece, static_cast<long long>(V)));
       if (tid == 0) s_found = 0x7fffffff;
