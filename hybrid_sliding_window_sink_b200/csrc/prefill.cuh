@@ -306,7 +306,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         it_kv += T;
       }
-      if (!ok) {   // let every issued copy land before the CTA can exit
+      // let every issued copy land before the CTA can exit (FIRST: in any case, so that a wait that
+      // gives up elsewhere leaves none behind)
+      if (!ok || FIRST) {
         if (it_q > 0) mbar_wait_drain(bar(kBarQFull), (it_q - 1) & 1, err);
         for (int s = 0; s < NKS; ++s)
           if (nk[s] > 0) mbar_wait_drain(bar(kBarKFull0 + s), (nk[s] - 1) & 1, err);

@@ -291,7 +291,9 @@ __global__ void __launch_bounds__(kGaThreads, 1)
           }
         }
       }
-      if (!ok) {   // let every issued copy land before the CTA can exit
+      // let every issued copy land before the CTA can exit (WIN: in any case, so that a wait that
+      // gives up elsewhere leaves none behind)
+      if (!ok || WIN) {
         if (nq > 0) mbar_wait_drain(bar(kGaQFull), (nq - 1) & 1, err);
         for (int t = nk - 2 < 0 ? 0 : nk - 2; t < nk; ++t)
           mbar_wait_drain(bar(kGaKFull + (t & 1)), (t >> 1) & 1, err);

@@ -241,10 +241,23 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
   const long long f1 = F * (blockIdx.x + 1) / gridDim.x;
   const int nqt = p.n_qtiles;
 
+  if constexpr (FIRST) {
+    // the first run's eight units before its block, one by each of the eight softmax warps (idle until
+    // the first product): forty copies issued by the producer alone held it for 7000 cycles
+    if (warp >= 6 && lane == 0) {
+      const int bg = static_cast<int>(f0 / nqt), b = bg / p.Hkv, g = bg - b * p.Hkv;
+      const int slot = warp - 6, u = static_cast<int>(f0 % nqt) + (p.q_off >> 4) - 8 + slot;
+      mbar_arrive_expect_tx(bar(kSwKVFull + slot), 16 * (kDQK + kDV) * 2);
+      for (int c = 0; c < 3; ++c)
+        tma_load_4d(sK + c * L::R_CHUNK + slot * L::UNIT_BYTES, &tmK, bar(kSwKVFull + slot), 64 * c, g, 16 * u, b);
+      for (int c = 0; c < 2; ++c)
+        tma_load_4d(sV + c * L::R_CHUNK + slot * L::UNIT_BYTES, &tmV, bar(kSwKVFull + slot), 64 * c, g, 16 * u, b);
+    }
+  }
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int seq = 0, nq = 0, nfirst = 0;
+      int seq = FIRST ? 8 : 0, nq = 0, nfirst = 0;   // (FIRST: the softmax warps brought the first eight)
       bool ok = true;
       auto load_unit = [&](int b, int g, int u) -> bool {
         const int slot = seq % kSwaUnits;
@@ -265,8 +278,18 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         const int bg = static_cast<int>(f / nqt), t = static_cast<int>(f % nqt);
         const int b = bg / p.Hkv, g = bg - b * p.Hkv;
         const int ua = t + (p.q_off >> 4);   // K/V unit holding the block's own positions
-        if (f == f0 || t == 0)
+        if ((!FIRST && f == f0) || (f != f0 && t == 0))
           for (int u = ua - 8; u < ua && ok; ++u) ok = load_unit(b, g, u);
+        if (!ok) break;
+        const int st = nq & 1;
+        if (nq >= 2 && !mbar_wait(bar(kSwQEmpty + st), ((nq >> 1) - 1) & 1, s_abort, err)) { ok = false; break; }
+        mbar_arrive_expect_tx(bar(kSwQFull + st), L::Q_STAGE);
+        for (int c = 0; c < 3; ++c)
+          tma_load_4d(sQ + st * L::Q_STAGE + c * L::Q_CHUNK, &tmQ, bar(kSwQFull + st), 64 * c,
+                      g * kSwaG, t * kSwaP, b);
+        SWA_TRACE(nq, 9);
+        ++nq;
+        ok = load_unit(b, g, ua);
         if constexpr (FIRST) {
           if (ok && (f == f0 || t == 0)) {   // keys 0 .. 15 of this sequence and KV head
             if (nfirst > 0) ok = mbar_wait(bar(kSwFirstFree), (nfirst - 1) & 1, s_abort, err);
@@ -280,18 +303,10 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
             }
           }
         }
-        if (!ok) break;
-        const int st = nq & 1;
-        if (nq >= 2 && !mbar_wait(bar(kSwQEmpty + st), ((nq >> 1) - 1) & 1, s_abort, err)) { ok = false; break; }
-        mbar_arrive_expect_tx(bar(kSwQFull + st), L::Q_STAGE);
-        for (int c = 0; c < 3; ++c)
-          tma_load_4d(sQ + st * L::Q_STAGE + c * L::Q_CHUNK, &tmQ, bar(kSwQFull + st), 64 * c,
-                      g * kSwaG, t * kSwaP, b);
-        SWA_TRACE(nq, 9);
-        ++nq;
-        ok = load_unit(b, g, ua);
       }
-      if (!ok) {   // let every issued copy land before the CTA can exit
+      // let every issued copy land before the CTA can exit (FIRST: in any case, so that a wait that
+      // gives up elsewhere leaves none behind)
+      if (!ok || FIRST) {
         for (int s = seq - kSwaUnits < 0 ? 0 : seq - kSwaUnits; s < seq; ++s)
           mbar_wait_drain(bar(kSwKVFull + s % kSwaUnits), (s / kSwaUnits) & 1, err);
         for (int i = nq - 2 < 0 ? 0 : nq - 2; i < nq; ++i)
@@ -460,7 +475,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       for (int i2 = 0; i2 < 4; ++i2) {
         const double ang = static_cast<double>((ctid >> 5) + 4 * i2) * s_invf[lane];
         const double nrev = rint(ang * 0.15915494309189535);
-        sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &turn[i2].y, &turn[i2].x);
+        __sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &turn[i2].y, &turn[i2].x);
       }
     }
     int seq = 0, i = 0, runs = 0;

@@ -32,7 +32,8 @@ def _status(lib):
     return lib.mimo_attn_device_status(ctypes.byref(word)), word.value
 
 
-CASES = [(640, 64, 8, 128, 4), (640, 64, 4, 200, 40), (300, 16, 4, 64, 9)]   # ring, pair, generic kernel
+CASES = [(640, 64, 8, 128, 4), (640, 64, 4, 200, 40), (300, 16, 4, 64, 9), (16, 8, 1, 128, 4),
+         (16, 16, 1, 8, 4)]   # ring, pair, generic kernel, and a single block of the first two
 
 
 def _run(x, dev, window, first):
