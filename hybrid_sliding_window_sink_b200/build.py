@@ -21,7 +21,7 @@ LIB_NAME = "libmimo_attn.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["mimo_attn.cu"]
 HEADERS = ["ptx.cuh", "decode.cuh", "decode_warp.cuh", "decode_fp8.cuh", "decode_mq_tma.cuh", "decode_mq.cuh", "select.cuh", "prefill.cuh", "prefill_swa.cuh", "prefill_ga.cuh",
-           "decode_paged.cuh", "append_paged.cuh", "verify.cuh"]
+           "prefill_first.cuh", "decode_paged.cuh", "append_paged.cuh", "verify.cuh"]
 
 
 def nvcc_path() -> str:

@@ -21,6 +21,7 @@
 #include "select.cuh"
 #include "prefill.cuh"
 #include "prefill_swa.cuh"
+#include "prefill_first.cuh"
 #include "prefill_ga.cuh"
 #include "decode_paged.cuh"
 #include "append_paged.cuh"
@@ -222,11 +223,12 @@ mimo_status launch_prefill(const mimo_shape* s, const void* q, const void* k, co
   return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
 }
 
-// SWA layer with 8 query heads per KV head, W <= 129, rot_dims <= 64: the ring kernel.
+// SWA layer with 8 query heads per KV head, W <= 129, rot_dims <= 64: the ring kernel; FIRST: with
+// first tokens (at most 16).
 template <bool FIRST = false>
 mimo_status launch_prefill_swa(const mimo_shape* s, const void* q, const void* k, const void* v,
                                PrefillParamsOf<FIRST> prm, int sms, cudaStream_t st) {
-  using L = mimo::SwaLayout<FIRST>;
+  using L = std::conditional_t<FIRST, mimo::SwaFirstLayout, mimo::SwaLayout>;
   CUtensorMap tq, tk, tv;
   const uint64_t n = static_cast<uint64_t>(s->seqlen), B = static_cast<uint64_t>(s->batch);
   const uint64_t nk = static_cast<uint64_t>(prm.nk);   // keys: n, or prefix + chunk
@@ -235,7 +237,11 @@ mimo_status launch_prefill_swa(const mimo_shape* s, const void* q, const void* k
       !make_tmap(&tk, k, mimo::kDQK, s->n_kv_heads, nk, B, 1, 16) ||
       !make_tmap(&tv, v, mimo::kDV, s->n_kv_heads, nk, B, 1, 16))
     return MIMO_ERR_CUDA;
-  if (cudaFuncSetAttribute(mimo::prefill_swa_kernel<FIRST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  constexpr auto kern = [] {
+    if constexpr (FIRST) return &mimo::prefill_swa_first_kernel;
+    else return &mimo::prefill_swa_kernel;
+  }();
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            L::SMEM) != cudaSuccess) {
     cudaGetLastError();
     return MIMO_ERR_CUDA;
@@ -245,7 +251,7 @@ mimo_status launch_prefill_swa(const mimo_shape* s, const void* q, const void* k
   if (work > 0x7fffffffLL) return MIMO_ERR_UNSUPPORTED;
   prm.num_work = static_cast<int>(work);
   const int grid = prm.num_work < sms ? prm.num_work : sms;
-  mimo::prefill_swa_kernel<FIRST><<<grid, mimo::kSwaThreads, L::SMEM, st>>>(tq, tk, tv, prm);
+  kern<<<grid, mimo::kSwaThreads, L::SMEM, st>>>(tq, tk, tv, prm);
   return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
 }
 

@@ -34,11 +34,6 @@
 // Each softmax group owns 256 TMEM columns: S in [0, 176), overwritten in place by P
 // (f16, two keys per column) in [0, 88), and O in [128, 256) (S is dead by then). The
 // PV MMA takes A = P from TMEM and B = V from the ring.
-// FIRST: the first n_first <= 16 tokens stay visible. They sit in one more unit behind the ring,
-// loaded once per (sequence, KV head) run: S has 192 columns, P lies in [0, 96). A key below a
-// row's window counts through that unit, one inside it through the ring, so none counts twice.
-// Every tile masks keys, so V rows that hold a NaN become zeros and their K rows NaN as they enter
-// (see v_row_not_finite in prefill.cuh; infinities are clamped).
 // Precision: rotated Q/K dims are stored as f16 and their QK^T k-steps run as f16 MMAs
 // (see prefill.cuh); P and V are f16 too (each V unit is converted in place once when it
 // enters the ring; P in [0, 1] keeps 11 significant bits instead of 8). P is scaled by the
@@ -68,16 +63,14 @@ constexpr int kSwaThreads = 448;
 constexpr int kSwaG = 8;            // query heads per KV head
 constexpr int kSwaP = 16;           // positions per row block
 constexpr int kSwaUnits = 11;       // 16-row units in the ring
+constexpr int kSwaR = 16 * kSwaUnits;
 constexpr int kSwaWin = 9;          // units holding the 144-key span of a row block
-constexpr int kSwaFirst = 16;       // most first tokens (one unit)
+constexpr int kSwaN = kSwaR;        // S columns: the whole ring, in slot order
 
-template <bool FIRST>
 struct SwaLayout {
-  static constexpr int UNITS = kSwaUnits + (FIRST ? 1 : 0);   // the ring, and the first tokens
-  static constexpr int N = 16 * UNITS;                 // S columns: all units, in slot order
   static constexpr int Q_CHUNK = 128 * 128;
   static constexpr int Q_STAGE = 3 * Q_CHUNK;
-  static constexpr int R_CHUNK = N * 128;              // 176 (192) rows x 64 dims
+  static constexpr int R_CHUNK = kSwaR * 128;          // 176 rows x 64 dims
   static constexpr int UNIT_BYTES = 16 * 128;          // one unit inside one 64-dim chunk
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + 2 * Q_STAGE;
@@ -88,8 +81,8 @@ struct SwaLayout {
   static constexpr int MISC_BYTES = 512 + 32 * 8;
   static constexpr int SMEM = OFF_MISC + MISC_BYTES + 1024;
   static constexpr uint32_t IDESC_PV = idesc_f16kind(128, 128, 0, 1, 1);   // P and V in f16
-  static constexpr uint32_t IDESC_S = idesc_bf16(128, N, 0, 0);
-  static constexpr uint32_t IDESC_S_F16 = idesc_f16kind(128, N, 0, 0, 1);   // rotated dims
+  static constexpr uint32_t IDESC_S = idesc_bf16(128, kSwaN, 0, 0);
+  static constexpr uint32_t IDESC_S_F16 = idesc_f16kind(128, kSwaN, 0, 0, 1);   // rotated dims
   static_assert(R_CHUNK % 1024 == 0, "ring chunks stay on swizzle atoms");
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -107,11 +100,7 @@ enum : int {
   kSwKVFull = 17,    // [11] unit landed
   kSwKReady = 28,    // [11] unit rotated (128 arrivals)
   kSwSlotFree = 39,  // [11] last MMA reading the unit finished
-  kSwFirstFull = 50,  // (FIRST) the first tokens' unit: landed, rotated (128 arrivals), free again
-  kSwFirstReady = 51,
-  kSwFirstFree = 52,
-  kSwTurn = 53,       // (FIRST) the turns of a run's start are in the spare table (128 arrivals)
-  kSwNumBars = 54
+  kSwNumBars = 50
 };
 
 // (x, y) <- (x cos - y sin, y cos + x sin) for two rotation pairs: xw and yw each hold two
@@ -184,11 +173,10 @@ __device__ __forceinline__ void rope_row_tab(uint8_t* row_base, int row, int nun
   rope_half(row_base, row, nun, t4, 2);
 }
 
-template <bool FIRST>
 __global__ void __launch_bounds__(kSwaThreads, 1)
     prefill_swa_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const PrefillParamsOf<FIRST> p) {
-  using L = SwaLayout<FIRST>;
+                       const __grid_constant__ CUtensorMap tmV, const PrefillParams p) {
+  using L = SwaLayout;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -209,7 +197,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
     for (int i = 0; i < kSwNumBars; ++i) {
       const bool many = (i >= kSwQReady && i < kSwQReady + 2) || (i >= kSwPReady && i < kSwPReady + 2) ||
                         (i >= kSwTmFree && i < kSwTab + 2) ||
-                        (i >= kSwKReady && i < kSwKReady + kSwaUnits) || i == kSwFirstReady || i == kSwTurn;
+                        (i >= kSwKReady && i < kSwKReady + kSwaUnits);
       mbar_init(bar(i), many ? 128u : 1u);
     }
     *s_abort = 0;
@@ -220,7 +208,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
     tmem_relinquish();
   }
   if (warp >= 2 && warp < 6 && threadIdx.x - 64 < half)
-    s_invf[threadIdx.x - 64] = inv_freq(p, threadIdx.x - 64);
+    s_invf[threadIdx.x - 64] = pow(p.rope_theta, -2.0 * (threadIdx.x - 64) / static_cast<double>(p.rot_dims));
   // the ring starts zeroed: slots outside a window are read (masked) before they are filled
   for (int o = threadIdx.x * 16; o < 3 * L::R_CHUNK + 2 * L::R_CHUNK; o += kSwaThreads * 16)
     *reinterpret_cast<uint4*>(smem + L::OFF_K + o) = make_uint4(0u, 0u, 0u, 0u);
@@ -241,23 +229,10 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
   const long long f1 = F * (blockIdx.x + 1) / gridDim.x;
   const int nqt = p.n_qtiles;
 
-  if constexpr (FIRST) {
-    // the first run's eight units before its block, one by each of the eight softmax warps (idle until
-    // the first product): forty copies issued by the producer alone held it for 7000 cycles
-    if (warp >= 6 && lane == 0) {
-      const int bg = static_cast<int>(f0 / nqt), b = bg / p.Hkv, g = bg - b * p.Hkv;
-      const int slot = warp - 6, u = static_cast<int>(f0 % nqt) + (p.q_off >> 4) - 8 + slot;
-      mbar_arrive_expect_tx(bar(kSwKVFull + slot), 16 * (kDQK + kDV) * 2);
-      for (int c = 0; c < 3; ++c)
-        tma_load_4d(sK + c * L::R_CHUNK + slot * L::UNIT_BYTES, &tmK, bar(kSwKVFull + slot), 64 * c, g, 16 * u, b);
-      for (int c = 0; c < 2; ++c)
-        tma_load_4d(sV + c * L::R_CHUNK + slot * L::UNIT_BYTES, &tmV, bar(kSwKVFull + slot), 64 * c, g, 16 * u, b);
-    }
-  }
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int seq = FIRST ? 8 : 0, nq = 0, nfirst = 0;   // (FIRST: the softmax warps brought the first eight)
+      int seq = 0, nq = 0;
       bool ok = true;
       auto load_unit = [&](int b, int g, int u) -> bool {
         const int slot = seq % kSwaUnits;
@@ -278,7 +253,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         const int bg = static_cast<int>(f / nqt), t = static_cast<int>(f % nqt);
         const int b = bg / p.Hkv, g = bg - b * p.Hkv;
         const int ua = t + (p.q_off >> 4);   // K/V unit holding the block's own positions
-        if ((!FIRST && f == f0) || (f != f0 && t == 0))
+        if (f == f0 || t == 0)
           for (int u = ua - 8; u < ua && ok; ++u) ok = load_unit(b, g, u);
         if (!ok) break;
         const int st = nq & 1;
@@ -290,28 +265,12 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         SWA_TRACE(nq, 9);
         ++nq;
         ok = load_unit(b, g, ua);
-        if constexpr (FIRST) {
-          if (ok && (f == f0 || t == 0)) {   // keys 0 .. 15 of this sequence and KV head
-            if (nfirst > 0) ok = mbar_wait(bar(kSwFirstFree), (nfirst - 1) & 1, s_abort, err);
-            if (ok) {
-              mbar_arrive_expect_tx(bar(kSwFirstFull), 16 * (kDQK + kDV) * 2);
-              for (int c = 0; c < 3; ++c)
-                tma_load_4d(sK + c * L::R_CHUNK + kSwaUnits * L::UNIT_BYTES, &tmK, bar(kSwFirstFull), 64 * c, g, 0, b);
-              for (int c = 0; c < 2; ++c)
-                tma_load_4d(sV + c * L::R_CHUNK + kSwaUnits * L::UNIT_BYTES, &tmV, bar(kSwFirstFull), 64 * c, g, 0, b);
-              ++nfirst;
-            }
-          }
-        }
       }
-      // let every issued copy land before the CTA can exit (FIRST: in any case, so that a wait that
-      // gives up elsewhere leaves none behind)
-      if (!ok || FIRST) {
+      if (!ok) {   // let every issued copy land before the CTA can exit
         for (int s = seq - kSwaUnits < 0 ? 0 : seq - kSwaUnits; s < seq; ++s)
           mbar_wait_drain(bar(kSwKVFull + s % kSwaUnits), (s / kSwaUnits) & 1, err);
         for (int i = nq - 2 < 0 ? 0 : nq - 2; i < nq; ++i)
           mbar_wait_drain(bar(kSwQFull + (i & 1)), (i >> 1) & 1, err);
-        if (FIRST && nfirst > 0) mbar_wait_drain(bar(kSwFirstFull), (nfirst - 1) & 1, err);
       }
     }
   } else if (warp == 1) {
@@ -323,8 +282,6 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       bool last_of[4] = {false, false, false, false};
       int s_useq = 0, kwait = 0;
       bool s_last = false, s_q = false, s_free = false, ok = true;
-      bool s_first = !FIRST;                   // the run's first tokens are in place
-      int runs = 0;
       auto prep_s = [&]() {
         const long long f = f0 + ns;
         const int t = static_cast<int>(f % nqt);
@@ -335,10 +292,6 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         kwait = first ? s_useq - 8 : s_useq;
         s_q = false;
         s_free = ns < 2;
-        if (FIRST && first) {
-          s_first = false;
-          ++runs;
-        }
       };
       if (ntiles > 0) prep_s();
       unsigned long long t_prog = globaltimer_ns();
@@ -352,8 +305,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
           while (s_q && kwait <= s_useq &&
                  mbar_test(bar(kSwKReady + kwait % kSwaUnits), (kwait / kSwaUnits) & 1))
             ++kwait;
-          if (!s_first) s_first = mbar_test(bar(kSwFirstReady), (runs - 1) & 1);
-          if (s_q && s_free && s_first && kwait > s_useq) {
+          if (s_q && s_free && kwait > s_useq) {
             SWA_TRACE(ns, 17);
             tc_fence_after();
             const uint32_t d = tmem + wg * 256;
@@ -381,31 +333,16 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
             tc_fence_after();
             const int uq = useq_of[npv & 3];
             const uint32_t base = tmem + wg * 256;
-            if constexpr (FIRST) {
-              // the first tokens' unit, then the nine of the window; not the two slots outside it: they
-              // may be taking rows of later keys, which are not f16 yet (and may hold anything)
-              umma_ts(base + 128, base + 8 * kSwaUnits, smem_desc(sV + kSwaUnits * L::UNIT_BYTES, L::R_CHUNK, 1024),
-                      L::IDESC_PV, 0u);
-              const int um = uq % kSwaUnits;
-              const uint32_t out2 = (1u << (um + 1 < kSwaUnits ? um + 1 : um + 1 - kSwaUnits)) |
-                                    (1u << (um + 2 < kSwaUnits ? um + 2 : um + 2 - kSwaUnits));
 #pragma unroll
-              for (int s2 = 0; s2 < kSwaUnits; ++s2)
-                if (!(out2 >> s2 & 1u))
-                  umma_ts(base + 128, base + 8 * s2, smem_desc(sV + s2 * L::UNIT_BYTES, L::R_CHUNK, 1024), L::IDESC_PV, 1u);
-            } else {
-#pragma unroll
-              for (int s2 = 0; s2 < kSwaUnits; ++s2) {
-                const uint64_t bd = smem_desc(sV + s2 * L::UNIT_BYTES, L::R_CHUNK, 1024);
-                umma_ts(base + 128, base + 8 * s2, bd, L::IDESC_PV, s2 > 0 ? 1u : 0u);
-              }
+            for (int s2 = 0; s2 < kSwaUnits; ++s2) {
+              const uint64_t bd = smem_desc(sV + s2 * L::UNIT_BYTES, L::R_CHUNK, 1024);
+              umma_ts(base + 128, base + 8 * s2, bd, L::IDESC_PV, s2 > 0 ? 1u : 0u);
             }
             umma_commit(bar(kSwPVDone + wg));
             umma_commit(bar(kSwSlotFree + (uq - 8) % kSwaUnits));
             if (last_of[npv & 3])
               for (int s2 = 1; s2 < kSwaWin; ++s2)
                 umma_commit(bar(kSwSlotFree + (uq - 8 + s2) % kSwaUnits));
-            if (FIRST && last_of[npv & 3]) umma_commit(bar(kSwFirstFree));
             SWA_TRACE(npv, 8);
             ++npv;
             prog = true;
@@ -435,50 +372,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       const bool w_ok = mbar_wait(b_, par, s_abort, err);
       return __all_sync(0xffffffffu, w_ok);
     };
-    // V rows of a unit (slot) of the ring: bf16 -> f16 in place; (FIRST) a NaN becomes 0 and a NaN
-    // in the key's K row, at dim 64 (the rotated dims are below it)
-    auto v_unit = [&](int slot) {
-      uint8_t* vb = smem + L::OFF_V + slot * L::UNIT_BYTES;
-      uint4 xv[2];
-#pragma unroll
-      for (int h2 = 0; h2 < 2; ++h2)
-        xv[h2] = *reinterpret_cast<const uint4*>(vb + h2 * L::R_CHUNK + ctid * 16);
-      if constexpr (FIRST) {
-        bool bad = false;
-#pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          uint32_t w[4] = {xv[h2].x, xv[h2].y, xv[h2].z, xv[h2].w};
-          bool nan = false;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
-            nan |= !__hbeq2(x, x);
-          }
-          if (nan) {
-            xv[h2] = make_uint4(0u, 0u, 0u, 0u);
-            bad = true;
-          }
-        }
-        const int row = ctid >> 3;
-        if (bad)
-          *reinterpret_cast<uint16_t*>(smem + L::OFF_K + L::R_CHUNK + slot * L::UNIT_BYTES + row * 128 + ((row & 7) << 4)) = kNan16;
-      }
-#pragma unroll
-      for (int h2 = 0; h2 < 2; ++h2)
-        *reinterpret_cast<uint4*>(vb + h2 * L::R_CHUNK + ctid * 16) =
-            make_uint4(bf16x2_to_f16x2(xv[h2].x), bf16x2_to_f16x2(xv[h2].y),
-                       bf16x2_to_f16x2(xv[h2].z), bf16x2_to_f16x2(xv[h2].w));
-    };
-    float2 turn[4];   // (FIRST) (cos, sin)(j w_lane) of positions j = warp, warp + 4, .. of a block
-    if (FIRST && half == 32) {
-#pragma unroll
-      for (int i2 = 0; i2 < 4; ++i2) {
-        const double ang = static_cast<double>((ctid >> 5) + 4 * i2) * s_invf[lane];
-        const double nrev = rint(ang * 0.15915494309189535);
-        __sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &turn[i2].y, &turn[i2].x);
-      }
-    }
-    int seq = 0, i = 0, runs = 0;
+    int seq = 0, i = 0;
     for (long long f = f0; f < f1; ++f, ++i) {
       const int t = static_cast<int>(f % nqt);
       const bool first = (f == f0 || t == 0);
@@ -488,19 +382,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       float* tab = reinterpret_cast<float*>(smem + L::OFF_TAB + (i & 1) * L::TAB_BYTES);
       if (ctid == 0) SWA_TRACE(i, 0);
       // (cos, sin) of the block's 16 positions (double buffered: tile i - 1 may still read)
-      if (FIRST && half == 32) {
-        // one angle per thread (frequency = lane), turned by the four positions the thread serves
-        const double ang = static_cast<double>(p0) * s_invf[lane];
-        const double nrev = rint(ang * 0.15915494309189535);
-        float sn, cs;
-        __sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &sn, &cs);
-#pragma unroll
-        for (int i2 = 0; i2 < 4; ++i2) {
-          float* tk = tab + ((ctid >> 5) + 4 * i2) * 64 + (lane >> 1) * 4 + (lane & 1);
-          tk[0] = cs * turn[i2].x - sn * turn[i2].y;
-          tk[2] = sn * turn[i2].x + cs * turn[i2].y;
-        }
-      } else if (half > 0) {
+      if (half > 0) {
         for (int e = ctid; e < kSwaP * half; e += 128) {
           const int pp = e / half, k = e - pp * half;
           const double ang = static_cast<double>(p0 + pp) * s_invf[k];
@@ -511,8 +393,6 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
           tk[0] = cs;
           tk[2] = sn;
         }
-      }
-      if (half > 0) {
         mbar_arrive(bar(kSwTab + (i & 1)));   // (bounded waits only: no hardware named barrier)
         if (!wait_all(bar(kSwTab + (i & 1)), (i >> 1) & 1)) break;
       }
@@ -526,74 +406,20 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       const int s_first = first ? useq - 8 : useq;
       for (int s = s_first; s <= useq && ok; ++s) ok = wait_all(bar(kSwKVFull + s % kSwaUnits), (s / kSwaUnits) & 1);
       if (!ok) break;
-      for (int s = s_first; s <= useq; ++s) v_unit(s % kSwaUnits);   // V units entering the ring
-      if constexpr (FIRST) {
-        if (first) {                                 // and the first tokens' unit of a new run
-          if (!wait_all(bar(kSwFirstFull), runs & 1)) break;
-          v_unit(kSwaUnits);
-          if (half == 32) {
-            // K of the window's units and of the first tokens, two units per turn: thread (row, 16-byte
-            // unit) takes the angles of its unit's first position from the lanes (frequency = lane) and
-            // turns them by its row's. The turns j w_k (see `turn`) are handed around in the table that
-            // the next block will write (its last reader was the previous block).
-            float* spare = reinterpret_cast<float*>(smem + L::OFF_TAB + ((i + 1) & 1) * L::TAB_BYTES);
+      for (int s = s_first; s <= useq; ++s) {   // V units entering the ring: bf16 -> f16 in place
+        uint8_t* vb = smem + L::OFF_V + (s % kSwaUnits) * L::UNIT_BYTES;
+        uint4 xv[2];
 #pragma unroll
-            for (int i2 = 0; i2 < 4; ++i2) {
-              float* tk = spare + ((ctid >> 5) + 4 * i2) * 64 + (lane >> 1) * 4 + (lane & 1);
-              tk[0] = turn[i2].x;
-              tk[2] = turn[i2].y;
-            }
-            mbar_arrive(bar(kSwTurn));
-            if (!wait_all(bar(kSwTurn), runs & 1)) break;
-            const int row = (ctid >> 2) & 15, u = ctid & 3;
-            const float4* t4 = reinterpret_cast<const float4*>(spare + row * 64);
-#pragma unroll 1
-            for (int k2 = ctid >> 6; k2 <= kSwaWin; k2 += 2) {   // 0 .. 8: the window's, 9: the first tokens'
-              const bool own = k2 < kSwaWin;
-              const int kpos0 = own ? p0 - 128 + 16 * k2 : 0, kpos = kpos0 + row;
-              const int ring_row = (own ? (s_first + k2) % kSwaUnits : kSwaUnits) * 16 + row;
-              const double ang = static_cast<double>(kpos0) * s_invf[lane];
-              const double nrev = rint(ang * 0.15915494309189535);
-              float bs, bc;
-              __sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &bs, &bc);
-              const bool raw = kpos >= p.krot_from && kpos < p.nk, cooked = kpos >= 0 && kpos < p.krot_from;
-              uint4* px = reinterpret_cast<uint4*>(smem + L::OFF_K + ring_row * 128 + ((u ^ (row & 7)) << 4));
-              uint4* py = reinterpret_cast<uint4*>(smem + L::OFF_K + ring_row * 128 + (((u + 4) ^ (row & 7)) << 4));
-              const uint4 x = *px, y = *py;
-              uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        for (int h2 = 0; h2 < 2; ++h2)
+          xv[h2] = *reinterpret_cast<const uint4*>(vb + h2 * L::R_CHUNK + ctid * 16);
 #pragma unroll
-              for (int e2 = 0; e2 < 4; ++e2) {
-                const int k = u * 8 + 2 * e2;
-                const float4 t = t4[u * 4 + e2];
-                const float c0 = __shfl_sync(0xffffffffu, bc, k), s0 = __shfl_sync(0xffffffffu, bs, k);
-                const float c1 = __shfl_sync(0xffffffffu, bc, k + 1), s1 = __shfl_sync(0xffffffffu, bs, k + 1);
-                if (raw) {
-                  rot_pair(xs[e2], ys[e2], make_float4(c0 * t.x - s0 * t.z, c1 * t.y - s1 * t.w,
-                                                       s0 * t.x + c0 * t.z, s1 * t.y + c1 * t.w));
-                } else if (cooked) {
-                  xs[e2] = bf16x2_to_f16x2(xs[e2]);
-                  ys[e2] = bf16x2_to_f16x2(ys[e2]);
-                }
-              }
-              if (raw || cooked) {
-                *px = make_uint4(xs[0], xs[1], xs[2], xs[3]);
-                *py = make_uint4(ys[0], ys[1], ys[2], ys[3]);
-              }
-            }
-          } else if (half > 0 && ctid < 16) {
-            const int ring_row = kSwaUnits * 16 + ctid;
-            if (ctid >= p.krot_from && ctid < p.nk) rope_row(sK, L::R_CHUNK, ring_row, ctid, p.rot_dims, s_invf);
-            else if (ctid < p.krot_from) f16_row(sK, L::R_CHUNK, ring_row, p.rot_dims);
-          }
-          ++runs;
-          fence_proxy_async_smem();
-          mbar_arrive(bar(kSwFirstReady));
-        }
+        for (int h2 = 0; h2 < 2; ++h2)
+          *reinterpret_cast<uint4*>(vb + h2 * L::R_CHUNK + ctid * 16) =
+              make_uint4(bf16x2_to_f16x2(xv[h2].x), bf16x2_to_f16x2(xv[h2].y),
+                         bf16x2_to_f16x2(xv[h2].z), bf16x2_to_f16x2(xv[h2].w));
       }
       if (half > 0) {
-        if (FIRST && first && half == 32) {
-          // done above
-        } else if (first) {
+        if (first) {
           for (int rr = ctid; rr < 16 * kSwaWin; rr += 128) {
             const int kpos = p0 - 128 + rr;
             const int ring_row = ((s_first + rr / 16) % kSwaUnits) * 16 + (rr & 15);
@@ -650,12 +476,6 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       const int um = useq % kSwaUnits;
       // 0 = empty, 1 = partial, 2 = full; elo/ehi: valid e of this row (partial blocks)
       auto block_class = [&](int c, int& elo, int& ehi) -> int {
-        if (FIRST && c == kSwaUnits) {   // first tokens below this row's window
-          elo = 0;
-          const int nfirst = first_of(p);
-          ehi = min(nfirst, klo) - 1;
-          return min(nfirst, klo_max) <= 0 ? 0 : (min(nfirst, klo_min) >= 16 ? 2 : 1);
-        }
         int d = um - c;
         d += d < 0 ? kSwaUnits : 0;
         const int kb = p0 - 16 * d;
@@ -667,11 +487,44 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       if (!wait_all(bar(kSwSFull + w), (i >> 1) & 1)) break;
       tc_fence_after();
       if (ctid == 0) SWA_TRACE(i, 3);
-      float ref = 0.f;                                      // reference of P (log2 units)
+      // pass 1: row max over the valid keys (four slot blocks per TMEM round trip)
+      float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < kSwaUnits; c += 2) {
+        uint32_t v[2][16];
+        int elo[2], ehi[2], k[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          k[q] = c + q < kSwaUnits ? block_class(c + q, elo[q], ehi[q]) : 0;
+          if (k[q]) tmem_ld16(trow + (c + q) * 16, v[q]);
+        }
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float mq = -INFINITY;
+          if (k[q] == 2) {
+            float mb = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              mq = fmax3_v(mq, __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
+              mb = fmax3_v(mb, __uint_as_float(v[q][e + 2]), __uint_as_float(v[q][e + 3]));
+            }
+            mq = fmaxf(mq, mb);
+          } else if (k[q] == 1) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e >= elo[q] && e <= ehi[q]) mq = fmaxf(mq, __uint_as_float(v[q][e]));
+          }
+          if (q & 1) mx1 = fmaxf(mx1, mq); else mx0 = fmaxf(mx0, mq);
+        }
+      }
+      const float mx = fmaxf(mx0, mx1);
+      const float amax = mx * p.scale_log2;                 // -inf when the row has no key
+      const float ref = amax == -INFINITY ? 0.f : amax;
+      // pass 2: P = exp2(a - amax) (0 outside the window), packed f16 into the S columns
       float sum0 = 0.f, sum1 = 0.f;
       // P of one slot block into pk; returns its sum
-      const unsigned long long sc2 = f2_pack(p.scale_log2, p.scale_log2);
-      unsigned long long nref2 = 0;
+      const unsigned long long sc2 = f2_pack(p.scale_log2, p.scale_log2), nref2 = f2_pack(-ref, -ref);
       auto p_block = [&](const uint32_t (&v)[16], int k, int elo, int ehi, uint32_t (&pk)[8]) -> float {
         if (k == 0) {
 #pragma unroll
@@ -694,138 +547,23 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         const float2 sab = f2_unpack(acc);
         return sab.x + sab.y;
       };
-      if constexpr (FIRST) {
-        // One pass over the slot blocks, one block per turn. The reference is the maximum of the first
-        // block that holds a key of the row, rounded up to a whole step, and moves only when a later
-        // block lies 2^8 above it (the P written so far are then scaled by a power of two, so exactly;
-        // rare). P = 2^(a - ref) stays within 2^8 of 1 at its largest, which f16 carries with all its 11
-        // bits. A pass of its own for the maximum cost six TMEM round trips more; two blocks per turn, in
-        // variants for full and partial ones, more code than the instruction caches of an SM that runs
-        // four different roles hold (stalls for instructions doubled). n = 32768, 64/8 heads, one after
-        // the other under the power cap: two passes 553 us, pairs in one pass 573 (cold 515), with their
-        // loads ahead 620, this 461 (cold 411).
-        ref = -INFINITY;
-        uint32_t v[16];
-        int elo, ehi;
-        tmem_ld16(trow, v);
 #pragma unroll 1
-        for (int c = 0; c < L::UNITS; ++c) {
-          tmem_wait_ld();
-          reg_fence16(v);
-          float x[16];
+      for (int c = 0; c < kSwaUnits; c += 2) {
+        uint32_t v[2][16];
+        int elo[2], ehi[2], k[2];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]);
-          // the next block's scores are under way while this one is worked on (P of block c ends at
-          // column 8 (c + 1), below them)
-          if (c + 1 < L::UNITS) tmem_ld16(trow + (c + 1) * 16, v);
-          const int kind = block_class(c, elo, ehi);
-          if (kind == 0) {                                  // no key for any row (the same for the tile)
-            const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-            tmem_st8(trow + c * 8, zero);
-            continue;
-          }
-          if (kind == 1) {                                  // masked keys to -inf
-            const uint32_t valid = ((1u << (ehi + 1)) - 1u) & ~((1u << elo) - 1u);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = valid >> e & 1u ? x[e] : -INFINITY;
-          }
-          float ma = fmax3(x[0], x[1], x[2]), mb = fmax3(x[3], x[4], x[5]);
-          ma = fmax3(ma, x[6], x[7]);
-          mb = fmax3(mb, x[8], x[9]);
-          ma = fmax3(ma, x[10], x[11]);
-          mb = fmax3(mb, x[12], x[13]);
-          const float pm = fmaxf(fmax3(ma, x[14], x[15]), mb) * p.scale_log2;
-          const bool move = pm > ref + 8.f;                 // (also the first key of the row)
-          const float was = ref;
-          ref = move ? ceilf(pm) : ref;                     // whole steps: scaling P is exact
-          if (__any_sync(0xffffffffu, move && was != -INFINITY)) {
-            const float al = move && was != -INFINITY ? ex2(was - ref) : 1.f;
-            sum0 *= al;
-            sum1 *= al;
-            const __half2 al2 = __float2half2_rn(al);
-            tmem_wait_st();
-#pragma unroll 1
-            for (int c2 = 0; c2 < c; ++c2) {
-              uint32_t w2[8];
-              tmem_ld8(trow + c2 * 8, w2);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&w2[e]), al2);
-                w2[e] = *reinterpret_cast<const uint32_t*>(&a);
-              }
-              tmem_st8(trow + c2 * 8, w2);
-            }
-          }
-          const float r0 = ref == -INFINITY ? 0.f : ref;
-          nref2 = f2_pack(-r0, -r0);
-          uint32_t pk[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 y = f2_unpack(f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), sc2, nref2));
-            const float a0 = ex2(y.x), a1 = ex2(y.y);
-            sum0 += a0;
-            sum1 += a1;
-            pk[e] = pack_f16(a0, a1);
-          }
-          tmem_st8(trow + c * 8, pk);
+        for (int q = 0; q < 2; ++q) {
+          k[q] = c + q < kSwaUnits ? block_class(c + q, elo[q], ehi[q]) : 0;
+          if (k[q]) tmem_ld16(trow + (c + q) * 16, v[q]);
         }
-        ref = ref == -INFINITY ? 0.f : ref;                 // a row without keys
-      } else {
-        // pass 1: row max over the valid keys (four slot blocks per TMEM round trip)
-        float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < L::UNITS; c += 2) {
-          uint32_t v[2][16];
-          int elo[2], ehi[2], k[2];
+        tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            k[q] = c + q < L::UNITS ? block_class(c + q, elo[q], ehi[q]) : 0;
-            if (k[q]) tmem_ld16(trow + (c + q) * 16, v[q]);
-          }
-          tmem_wait_ld();
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float mq = -INFINITY;
-            if (k[q] == 2) {
-              float mb = -INFINITY;
-#pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                mq = fmax3_v(mq, __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
-                mb = fmax3_v(mb, __uint_as_float(v[q][e + 2]), __uint_as_float(v[q][e + 3]));
-              }
-              mq = fmaxf(mq, mb);
-            } else if (k[q] == 1) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (e >= elo[q] && e <= ehi[q]) mq = fmaxf(mq, __uint_as_float(v[q][e]));
-            }
-            if (q & 1) mx1 = fmaxf(mx1, mq); else mx0 = fmaxf(mx0, mq);
-          }
-        }
-        const float mx = fmaxf(mx0, mx1);
-        const float amax = mx * p.scale_log2;                 // -inf when the row has no key
-        ref = amax == -INFINITY ? 0.f : amax;
-        nref2 = f2_pack(-ref, -ref);
-        // pass 2: P = exp2(a - amax) (0 outside the window), packed f16 into the S columns
-#pragma unroll 1
-        for (int c = 0; c < L::UNITS; c += 2) {
-          uint32_t v[2][16];
-          int elo[2], ehi[2], k[2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            k[q] = c + q < L::UNITS ? block_class(c + q, elo[q], ehi[q]) : 0;
-            if (k[q]) tmem_ld16(trow + (c + q) * 16, v[q]);
-          }
-          tmem_wait_ld();
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            if (c + q < L::UNITS) {
-              uint32_t pk[8];
-              const float sq = p_block(v[q], k[q], elo[q], ehi[q], pk);
-              if (q & 1) sum1 += sq; else sum0 += sq;
-              tmem_st8(trow + (c + q) * 8, pk);
-            }
+        for (int q = 0; q < 2; ++q) {
+          if (c + q < kSwaUnits) {
+            uint32_t pk[8];
+            const float sq = p_block(v[q], k[q], elo[q], ehi[q], pk);
+            if (q & 1) sum1 += sq; else sum0 += sq;
+            tmem_st8(trow + (c + q) * 8, pk);
           }
         }
       }
@@ -843,8 +581,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       if (!wait_all(bar(kSwPVDone + w), (i >> 1) & 1)) break;
       tc_fence_after();
       if (ctid == 0) SWA_TRACE(i, 5);
-      const bool none = FIRST ? lt == 0.f : !(lt > 0.f);   // no key and no sink (FIRST: a NaN stays one)
-      const float inv_l = none ? 0.f : sc / lt;
+      const float inv_l = lt > 0.f ? sc / lt : 0.f;
       __nv_bfloat16* orow = p.out + ((static_cast<long long>(b) * p.n + qi) * p.Hq + hq) * 128;
       // O columns [128, 192) overlap the S columns of this group's next tile: read them
       // first, release the TMEM region, then finish with columns [192, 256)
@@ -876,7 +613,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       }
       if (row_ok && p.lse)
         p.lse[(static_cast<long long>(b) * p.Hq + hq) * p.n + qi] =
-            none ? -INFINITY : (M + log2f(lt)) * kLn2;
+            lt > 0.f ? (M + log2f(lt)) * kLn2 : -INFINITY;
       if (ctid == 0) SWA_TRACE(i, 6);
     }
   }
