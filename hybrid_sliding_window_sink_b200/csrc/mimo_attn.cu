@@ -1325,7 +1325,7 @@ mimo_status mimo_attn_verify_drafts(int batch, int n_drafts, int vocab, int prob
   prm.T = n_drafts;
   prm.V = vocab;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // 16-byte loads where every row starts on 16 bytes
+  // aligned 16-byte loads where every row starts on 16 bytes (see vf_piece)
   const int per16 = probs_type == MIMO_PROBS_F32 ? 4 : 8;
   const bool vec = vocab % per16 == 0 && aligned(prm.p, 16) && aligned(prm.q, 16);
   if (probs_type == MIMO_PROBS_F32)

@@ -7,8 +7,8 @@
 //   accepted a = the first t with not (u_t q_t(x_t) < p_t(x_t)), or n;
 //   w(v) = max(p_a(v) - q_a(v), 0) for a < n, p_n(v) for a = n;
 //   next token = the smallest v with w(0) + .. + w(v) > u_T * sum w.
-// u q and p - q of fp32 values are exact in double, and the sums are double: at V = 131072 an
-// fp32 running sum is off by about as much as one token weighs (1e-5).
+// u q is exact in double. The sums are pairs of floats (see VfSum) within a lane and double across
+// lanes: at V = 131072 an fp32 running sum is off by about as much as one token weighs (1e-5).
 //
 // Work: one row of p and one of q per sequence, read once (the accepted rows are only probed at
 // x_t), so the bytes bound it; for few sequences the latency of the steps does. A cluster of C
@@ -108,48 +108,91 @@ struct VfSum {
   __device__ __forceinline__ double get() const { return static_cast<double>(s) + static_cast<double>(c); }
 };
 
-// Sum of the weights of [v0, v1) by one warp (each lane returns its share). VEC: 16-byte loads,
-// which need rows that start on 16 bytes (V a multiple of W); otherwise one value per lane and
-// load, eight loads in flight.
+// Sixteen bytes that start `off` bytes into two neighbouring vectors.
+__device__ __forceinline__ uint4 vf_shift(const uint4& lo, const uint4& hi, int off) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+  const int bits = (off & 3) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// Sum of the weights of [v0, v1) by one warp (each lane returns its share). VEC: rows start on 16
+// bytes (V a multiple of W) and come by 16-byte loads. Otherwise fp32 rows take one value per lane and
+// load, eight loads in flight; for bf16 those move too few bytes: its 16-byte loads follow p's
+// alignment, a vector of q is put together from the two that hold it, and the ends of the piece (fewer
+// than 2 W values each), where a load would reach past the piece, go one value per lane. 64 rows of
+// 131071: fp32 18.4 us by values, 21.5 by vectors; bf16 23.6 and 17.2 (16 x 50021 alone: 8.7 and 7.3).
 template <typename E, bool VEC>
 __device__ __forceinline__ double vf_piece(const E* p, const E* q, int hot, int v0, int v1) {
   using X = VfVec<E>;
   const int lane = threadIdx.x & 31;
+  constexpr int W = X::W, U = X::U;
   VfSum sum[2];
-  if constexpr (VEC) {
-    constexpr int W = X::W, U = X::U;
-    for (int v = v0 + lane * W; v < v1; v += 32 * W * U) {
-      uint4 a[U], b[U];
+  if constexpr (!VEC && sizeof(E) == 4) {
+    constexpr int N = 8;
+    for (int v = v0 + lane; v < v1; v += 32 * N) {
+      float x[N], y[N];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int at = v + u * 32 * W;
-        a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (at < v1) {
-          a[u] = __ldg(reinterpret_cast<const uint4*>(p + at));
-          if (q) b[u] = __ldg(reinterpret_cast<const uint4*>(q + at));
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float x[W], y[W];
-        X::get(a[u], x);
-        X::get(b[u], y);
-#pragma unroll
-        for (int e = 0; e < W; ++e) sum[e & 1].add(x[e], v + u * 32 * W + e == hot ? 1.f : y[e]);
-      }
-    }
-  } else {
-    constexpr int U = 8;
-    for (int v = v0 + lane; v < v1; v += 32 * U) {
-      float x[U], y[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
+      for (int u = 0; u < N; ++u) {
         const int at = v + u * 32;
         x[u] = at < v1 ? vf_load(p + at) : 0.f;
         y[u] = at < v1 && q ? vf_load(q + at) : 0.f;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) sum[u & 1].add(x[u], v + u * 32 == hot ? 1.f : y[u]);
+      for (int u = 0; u < N; ++u) sum[u & 1].add(x[u], v + u * 32 == hot ? 1.f : y[u]);
+    }
+    return sum[0].get() + sum[1].get();
+  }
+  int s0 = v0, s1 = v1, off = 0;              // whole vectors: [s0, s1); bytes q starts after one there
+  if constexpr (!VEC) {
+    auto past = [](const E* x) { return static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15); };
+    s0 += ((16 - past(p + v0)) & 15) / static_cast<int>(sizeof(E));
+    int over = 0;                             // values of q's second vector behind the last one of p
+    if (q) {
+      off = past(q + s0);
+      const int before = off / static_cast<int>(sizeof(E));
+      if (before) {
+        if (s0 - before < v0) s0 += W;
+        over = W - before;
+      }
+    }
+    s1 = v1 - s0 - over >= W ? s0 + (v1 - s0 - over) / W * W : s0;
+    if (s0 > v1) s0 = s1 = v1;
+    for (int part = 0; part < 2; ++part) {
+      const int v = (part ? s1 : v0) + lane;
+      if (v < (part ? v1 : s0)) sum[part].add(vf_load(p + v), v == hot ? 1.f : q ? vf_load(q + v) : 0.f);
+    }
+  }
+  for (int v = s0 + lane * W; v < s1; v += 32 * W * U) {
+    uint4 a[U], b[U], c[VEC ? 1 : U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = v + u * 32 * W;
+      a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (!VEC) c[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (at < s1) {
+        a[u] = __ldg(reinterpret_cast<const uint4*>(p + at));
+        if constexpr (VEC) {
+          if (q) b[u] = __ldg(reinterpret_cast<const uint4*>(q + at));
+        } else if (q) {
+          const uint4* qa = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(q + at) - off);
+          b[u] = __ldg(qa);
+          if (off) c[u] = __ldg(qa + 1);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (!VEC) b[u] = vf_shift(b[u], c[u], off);
+      float x[W], y[W];
+      X::get(a[u], x);
+      X::get(b[u], y);
+#pragma unroll
+      for (int e = 0; e < W; ++e) sum[e & 1].add(x[e], v + u * 32 * W + e == hot ? 1.f : y[e]);
     }
   }
   return sum[0].get() + sum[1].get();

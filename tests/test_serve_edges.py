@@ -115,3 +115,27 @@ def test_python_marshalling_of_every_call(cuda_device, monkeypatch):
     monkeypatch.setattr(_lib, "_usual", lambda: False)
     slow = everything()
     assert len(fast) == len(slow) and all(torch.equal(a, b) for a, b in zip(fast, slow))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [1, 7, 8, 9, 255, 257, 2049, 4099, 20005])
+@pytest.mark.parametrize("shift", [0, 1, 3, 7])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_verify_rows_at_any_alignment(cuda_device, V, shift, dtype):
+    """Rows of p and q that start anywhere between two 16-byte borders, inside larger buffers whose
+    neighbours would win if they were read as part of a row."""
+    B, T = 5, 3
+    g = torch.Generator().manual_seed(V + 31 * shift)
+    n_p, n_q = B * (T + 1) * V, B * T * V
+    base_p, base_q = (torch.full((n + 32,), 1e30, dtype=dtype, device=cuda_device) for n in (n_p, n_q))
+    p = base_p[shift:shift + n_p].view(B, T + 1, V)
+    q = base_q[2 * shift + 1:2 * shift + 1 + n_q].view(B, T, V)
+    p.copy_(torch.softmax(torch.randn(B, T + 1, V, generator=g), -1))
+    q.copy_(torch.softmax(torch.randn(B, T, V, generator=g), -1))
+    draft = torch.randint(0, V, (B, T), generator=g).int()
+    u = torch.rand(B, T + 1, generator=g)
+    for given in (q, None):
+        acc, tok = _lib.verify_drafts(p, draft.to(cuda_device), u.to(cuda_device), given)
+        want = serve.verify_drafts(wl.to_f64(p.cpu()), None if given is None else wl.to_f64(q.cpu()),
+                                   draft.numpy(), wl.to_f64(u))
+        assert acc.tolist() == want[0].tolist() and tok.tolist() == want[1].tolist()
