@@ -93,7 +93,7 @@ def build_binding(force: bool = False) -> str:
            "-I", INCLUDE, "-I", sysconfig.get_path("include"), "-isystem", os.path.join(cuda, "include")]
     for d in cpp_extension.include_paths():
         cmd += ["-isystem", d]
-    cmd += [src, "-o", path + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+    cmd += [src, "-o", path + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-ltorch_cuda"]
     subprocess.run(cmd, check=True)
     os.replace(path + ".tmp", path)
     return path

@@ -10,6 +10,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -120,6 +122,12 @@ bool pool(const at::Tensor& t, long long& stride) {
   return true;
 }
 
+// A new tensor on t's device, without the dispatcher (and scratch straight from the allocator): one
+// short paged decode 9.4 -> 8.4 us a call, a small verification 6.6 -> 6.2.
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor& t) {
+  return at::Tensor(at::detail::empty_cuda(sizes, type, t.device(), std::nullopt));
+}
+
 PyObject* pair(at::Tensor a, const at::Tensor* b) {
   PyObject* x = THPVariable_Wrap(std::move(a));
   PyObject* y = b ? THPVariable_Wrap(*b) : Py_NewRef(Py_None);
@@ -134,14 +142,15 @@ PyObject* pair(at::Tensor a, const at::Tensor* b) {
   return r;
 }
 
-// Runs f with C++ exceptions turned into Python's.
+// Runs f; a C++ exception (no memory for an output, say) is one more call that is not usual: _lib.py
+// makes it again and raises torch's own error.
 template <typename F>
 PyObject* guarded(F f) {
   try {
     return f();
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
+  } catch (const std::exception&) {
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
   }
 }
 
@@ -180,13 +189,13 @@ PyObject* decode_paged(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const mimo_pages pages{static_cast<const int*>(table->data_ptr()), static_cast<int>(table->size(1)),
                            static_cast<int>(N), static_cast<int>(page), stride};
     const size_t bytes = fn.workspace_size(&shape, &pages, window, first);
-    at::Tensor out = at::empty({B, hq, 128}, q->options());
-    at::Tensor lse, ws;
-    if (in.flag(11)) lse = at::empty({B, hq}, q->options().dtype(at::kFloat));
-    if (bytes) ws = at::empty({static_cast<int64_t>(bytes)}, q->options().dtype(at::kByte));
+    at::Tensor out = fresh({B, hq, 128}, at::kBFloat16, *q), lse;
+    if (in.flag(11)) lse = fresh({B, hq}, at::kFloat, *q);
+    c10::DataPtr ws;                       // (goes back to the allocator in stream order)
+    if (bytes) ws = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
     void* st = c10::cuda::getCurrentCUDAStream().stream();
     float* l = lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr;
-    void* w = ws.defined() ? ws.data_ptr() : nullptr;
+    void* w = ws.get();
     const int* len = static_cast<const int*>(lengths->data_ptr());
     const float* sk = static_cast<const float*>(Args::data(sink));
     const mimo_status rc =
@@ -266,8 +275,8 @@ PyObject* prefill_first(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (!in.ok) Py_RETURN_NONE;
     const mimo_shape shape{static_cast<int>(B), static_cast<int>(len), static_cast<int>(hq), static_cast<int>(hkv), 192,
                            128, scale};
-    at::Tensor out = at::empty({B, len, hq, 128}, q->options()), lse;
-    if (in.flag(11)) lse = at::empty({B, hq, len}, q->options().dtype(at::kFloat));
+    at::Tensor out = fresh({B, len, hq, 128}, at::kBFloat16, *q), lse;
+    if (in.flag(11)) lse = fresh({B, hq, len}, at::kFloat, *q);
     const mimo_status rc = fn.prefill_first(
         &shape, q->data_ptr(), k->data_ptr(), v->data_ptr(), off, in.flag(7), static_cast<float*>(Args::data(sink)),
         window, first, theta, rot, out.data_ptr(), lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
@@ -294,7 +303,7 @@ PyObject* verify_drafts(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor* q = in.given(3) ? in.tensor(3, type, {B, T1 - 1, V}) : nullptr;
     const at::Tensor* valid = in.given(4) ? in.tensor(4, at::kInt, {B}) : nullptr;
     if (!in.ok) Py_RETURN_NONE;
-    at::Tensor acc = at::empty({B}, draft->options()), tok = at::empty({B, T1}, draft->options());
+    at::Tensor acc = fresh({B}, at::kInt, *draft), tok = fresh({B, T1}, at::kInt, *draft);
     const mimo_status rc = fn.verify(
         static_cast<int>(B), static_cast<int>(T1 - 1), static_cast<int>(V),
         type == at::kFloat ? MIMO_PROBS_F32 : MIMO_PROBS_BF16, p->data_ptr(), Args::data(q),
