@@ -80,6 +80,22 @@ int current_device() {
   return dev;
 }
 
+// f[d] = theta^(-2d/rot) for d < rot / 2, as products of at most four powers: off by less than 2^-49 of
+// itself (bases from 1e-3 to 1e7; the rounded exponent alone costs 2^-50), so that the angle at position
+// 2^24 turns by less than 2^-25. A pow for each of 32 made a short call 4.9 instead of 4.7 us.
+void inv_freqs(double theta, int rot, double* f) {
+  double low[8] = {1.0};
+  for (int j = 1; j < 8; ++j) {
+    const int top = j >= 4 ? 4 : j >= 2 ? 2 : 1;
+    low[j] = j == top ? std::pow(theta, -2.0 * j / rot) : low[top] * low[j - top];
+  }
+  double base = 1.0;
+  for (int d = 0; d < rot / 2; ++d) {
+    if (d && d % 8 == 0) base = std::pow(theta, -2.0 * d / rot);
+    f[d] = base * low[d % 8];
+  }
+}
+
 int sm_count_for(int dev) {
   if (dev < 0 || dev >= kMaxDevices) return 148;
   int v = g_sm_count[dev].load(std::memory_order_relaxed);
@@ -746,7 +762,7 @@ mimo_status run_prefill_chunk(const mimo_shape* s, const void* q, const void* k,
   const int group = s->n_q_heads / s->n_kv_heads;
   // without a window that ends inside the keys, the first tokens are visible anyway
   if (n_first > 0 && window > 0 && window < prm.nk) {
-    for (int d = 0; d < rot_dims / 2; ++d) prm.invf[d] = std::pow(prm.rope_theta, -2.0 * d / rot_dims);
+    inv_freqs(prm.rope_theta, rot_dims, prm.invf);
     switch (group) {
       case 1: return prefill_first_group<1>(s, q, k, v, prm, sms, st);
       case 2: return prefill_first_group<2>(s, q, k, v, prm, sms, st);
@@ -955,7 +971,7 @@ mimo_status run_append_paged(const mimo_shape* s, const void* k_new, const void*
   prm.max_pages = pg->max_pages;
   prm.num_pages = pg->num_pages;
   page_divisor(pg->page_size, prm.div_mul, prm.div_shift);
-  for (int d = 0; d < rot / 2; ++d) prm.invf[d] = std::pow(static_cast<double>(theta), -2.0 * d / rot);
+  inv_freqs(static_cast<double>(theta), rot, prm.invf);
   const size_t smem = static_cast<size_t>(prm.tokens) * (rot / 2) * sizeof(float2);   // <= 24 KB
   mimo::append_paged_kernel<FP8><<<static_cast<unsigned>(blocks), mimo::kApThreads, smem, static_cast<cudaStream_t>(stream)>>>(prm);
   return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
