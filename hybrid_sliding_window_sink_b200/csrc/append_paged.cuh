@@ -5,7 +5,7 @@
 // the angle pos * theta^(-2d/rot), reduced modulo 2 pi in double precision. FP8 rows: scale =
 // amax / 448 (1 for a row of zeros), byte = e4m3(x / scale), K from its rotated fp32 values.
 //
-// The bytes bound it (640 read and 640, or 328, written per row). A CTA takes kApTokens tokens
+// The bytes bound it (640 read and 640, or 328, written per row). A CTA takes a few tokens (32 rows)
 // of one sequence with all their heads: the (cos, sin) of a token is computed once for its heads
 // (the frequencies theta^(-2d/rot) come from the host), and half a warp writes a row: lane l its V
 // unit l (16 bytes) and, for l < 12, two K units, the partners u and u + rot/16 of the rotation where
