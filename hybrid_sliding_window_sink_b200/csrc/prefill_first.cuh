@@ -10,10 +10,15 @@
 //   * The softmax finds its reference on the way (one pass, one slot block per turn).
 //   * PV multiplies the window's nine units and the first tokens', not the two slots that may be
 //     taking rows of later keys.
-//   * Angles: a block's table from one angle per thread, a run's start from one per lane and unit.
+//   * Angles: a block's table from one angle per thread, a run's start from one per lane and unit. The
+//     first run's units are loaded, converted and rotated by the softmax warps, one each (n = 203, 8/1
+//     heads: 15.2 -> 11.8 us with the next).
+//   * K has no barrier of its own (Q of a block is handed over after the block's K and V), and a group
+//     hands over by one arrival per warp: a thousand arrivals at a run's start, and the nine polls of
+//     the issuer, took 2000 cycles.
 //   * Every tile masks keys, so a V row that holds a NaN becomes zeros and its K row a NaN as it enters
 //     (see v_row_not_finite in prefill.cuh; infinities are clamped).
-// Bound: bytes at n = 32768 (1.51 GB, 231 us at the measured copy rate); measured 411 us cold, 461 us under
+// Bound: bytes at n = 32768 (1.51 GB, 231 us at the measured copy rate); measured 405 us cold, 460 us under
 // the power cap (the kernel without first tokens 448 and 500). A trace puts the RoPE group and the two
 // softmax groups level at 6200 - 6500 cycles per row block, against 4000 at the byte floor.
 #pragma once
@@ -49,10 +54,10 @@ struct SwaFirstLayout {
 
 // Barriers beyond those of prefill_swa.cuh.
 enum : int {
-  kSwFirstFull = kSwNumBars,        // the first tokens' unit: landed, rotated (128 arrivals), free again
-  kSwFirstReady,
+  kSwFirstFull = kSwNumBars,        // the first tokens' unit: landed, free again
   kSwFirstFree,
-  kSwTurn,                          // the turns of a run's start are in the spare table (128 arrivals)
+  kSwTurn,                          // the turns of a run's start are in the spare table (4 arrivals)
+  kSwStart,                         // the softmax warps have the first run's first eight units ready (8)
   kSfNumBars
 };
 
@@ -78,10 +83,11 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSfNumBars; ++i) {
-      const bool many = (i >= kSwQReady && i < kSwQReady + 2) || (i >= kSwPReady && i < kSwPReady + 2) ||
-                        (i >= kSwTmFree && i < kSwTab + 2) ||
-                        (i >= kSwKReady && i < kSwKReady + kSwaUnits) || i == kSwFirstReady || i == kSwTurn;
-      mbar_init(bar(i), many ? 128u : 1u);
+      // one arrival per warp (of four) where a group hands something over; K needs no barrier of its
+      // own here: Q of a block is handed over after the block's K and V
+      const bool group = (i >= kSwQReady && i < kSwQReady + 2) || (i >= kSwPReady && i < kSwPReady + 2) ||
+                         (i >= kSwTmFree && i < kSwTmFree + 2) || (i >= kSwTab && i < kSwTab + 2) || i == kSwTurn;
+      mbar_init(bar(i), i == kSwStart ? 8u : group ? 4u : 1u);
     }
     *s_abort = 0;
     mbar_fence_init();
@@ -123,6 +129,77 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
     for (int c = 0; c < 2; ++c)
       tma_load_4d(sV + c * L::R_CHUNK + slot * L::UNIT_BYTES, &tmV, bar(kSwKVFull + slot), 64 * c, g, 16 * u, b);
   }
+  auto arrive_warp = [&](uint32_t b_) {       // everything this warp wrote before
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b_);
+  };
+  // V, sixteen bytes of each half of row x / 8 of a unit (slot) of the ring: bf16 -> f16 in place; a NaN
+  // becomes 0 and a NaN in the key's K row, at dim 64 (the rotated dims are below it)
+  auto v_part = [&](int slot, int x) {
+    uint8_t* vb = smem + L::OFF_V + slot * L::UNIT_BYTES;
+    uint4 xv[2];
+#pragma unroll
+    for (int h2 = 0; h2 < 2; ++h2)
+      xv[h2] = *reinterpret_cast<const uint4*>(vb + h2 * L::R_CHUNK + x * 16);
+    bool bad = false;
+#pragma unroll
+    for (int h2 = 0; h2 < 2; ++h2) {
+      uint32_t w[4] = {xv[h2].x, xv[h2].y, xv[h2].z, xv[h2].w};
+      bool nan = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 x2 = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
+        nan |= !__hbeq2(x2, x2);
+      }
+      if (nan) {
+        xv[h2] = make_uint4(0u, 0u, 0u, 0u);
+        bad = true;
+      }
+    }
+    const int row = x >> 3;
+    if (bad)
+      *reinterpret_cast<uint16_t*>(smem + L::OFF_K + L::R_CHUNK + slot * L::UNIT_BYTES + row * 128 + ((row & 7) << 4)) = kNan16;
+#pragma unroll
+    for (int h2 = 0; h2 < 2; ++h2)
+      *reinterpret_cast<uint4*>(vb + h2 * L::R_CHUNK + x * 16) =
+          make_uint4(bf16x2_to_f16x2(xv[h2].x), bf16x2_to_f16x2(xv[h2].y),
+                     bf16x2_to_f16x2(xv[h2].z), bf16x2_to_f16x2(xv[h2].w));
+  };
+  // K row x / 4 of a unit, 16-byte units x % 4 and that + 4: rotated (or, stored rotated, made f16). The
+  // angles of the unit's first position lie across the warp (bc, bs: frequency = lane) and are turned by
+  // the row's (see `turn`).
+  auto k_part = [&](int slot, int x, int kpos0, float bc, float bs, const float* turns) {
+    const int row = x >> 2, u = x & 3, kpos = kpos0 + row, ring_row = slot * 16 + row;
+    const float4* t4 = reinterpret_cast<const float4*>(turns + row * 64);
+    const bool raw = kpos >= p.krot_from && kpos < p.nk, cooked = kpos >= 0 && kpos < p.krot_from;
+    uint4* px = reinterpret_cast<uint4*>(smem + L::OFF_K + ring_row * 128 + ((u ^ (row & 7)) << 4));
+    uint4* py = reinterpret_cast<uint4*>(smem + L::OFF_K + ring_row * 128 + (((u + 4) ^ (row & 7)) << 4));
+    const uint4 xv = *px, yv = *py;
+    uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w}, ys[4] = {yv.x, yv.y, yv.z, yv.w};
+#pragma unroll
+    for (int e2 = 0; e2 < 4; ++e2) {
+      const int k = u * 8 + 2 * e2;
+      const float4 t = t4[u * 4 + e2];
+      const float c0 = __shfl_sync(0xffffffffu, bc, k), s0 = __shfl_sync(0xffffffffu, bs, k);
+      const float c1 = __shfl_sync(0xffffffffu, bc, k + 1), s1 = __shfl_sync(0xffffffffu, bs, k + 1);
+      if (raw) {
+        rot_pair(xs[e2], ys[e2], make_float4(c0 * t.x - s0 * t.z, c1 * t.y - s1 * t.w,
+                                             s0 * t.x + c0 * t.z, s1 * t.y + c1 * t.w));
+      } else if (cooked) {
+        xs[e2] = bf16x2_to_f16x2(xs[e2]);
+        ys[e2] = bf16x2_to_f16x2(ys[e2]);
+      }
+    }
+    if (raw || cooked) {
+      *px = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+      *py = make_uint4(ys[0], ys[1], ys[2], ys[3]);
+    }
+  };
+  auto angle = [&](int pos, float& sn, float& cs) {   // of frequency `lane`
+    const double ang = static_cast<double>(pos) * s_invf[lane];
+    const double nrev = rint(ang * 0.15915494309189535);
+    __sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &sn, &cs);
+  };
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -186,10 +263,9 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       int ns = 0, npv = 0, seq = 0;
       int useq_of[4] = {0, 0, 0, 0};
       bool last_of[4] = {false, false, false, false};
-      int s_useq = 0, kwait = 0;
+      int s_useq = 0;
       bool s_last = false, s_q = false, s_free = false, ok = true;
-      bool s_first = false;                    // the run's first tokens are in place
-      int runs = 0;
+      bool s_start = false;                    // the softmax warps' units of the first run are ready
       auto prep_s = [&]() {
         const long long f = f0 + ns;
         const int t = static_cast<int>(f % nqt);
@@ -197,13 +273,8 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         s_last = (f == f1 - 1 || t == nqt - 1);
         if (first) seq += 8;
         s_useq = seq++;
-        kwait = first ? s_useq - 8 : s_useq;
         s_q = false;
         s_free = ns < 2;
-        if (first) {
-          s_first = false;
-          ++runs;
-        }
       };
       if (ntiles > 0) prep_s();
       unsigned long long t_prog = globaltimer_ns();
@@ -214,11 +285,8 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
           const int wg = ns & 1;
           if (!s_q) s_q = mbar_test(bar(kSwQReady + wg), (ns >> 1) & 1);
           if (!s_free) s_free = mbar_test(bar(kSwTmFree + wg), ((ns >> 1) - 1) & 1);
-          while (s_q && kwait <= s_useq &&
-                 mbar_test(bar(kSwKReady + kwait % kSwaUnits), (kwait / kSwaUnits) & 1))
-            ++kwait;
-          if (!s_first) s_first = mbar_test(bar(kSwFirstReady), (runs - 1) & 1);
-          if (s_q && s_free && s_first && kwait > s_useq) {
+          if (!s_start) s_start = mbar_test(bar(kSwStart), 0);
+          if (s_q && s_free && s_start) {
             SWA_TRACE(ns, 17);
             tc_fence_after();
             const uint32_t d = tmem + wg * 256;
@@ -270,8 +338,8 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         }
         if (prog) {
           idle = 0;
-        } else if ((++idle & 1023u) == 0) {   // look at the clock only now and then
-          if (idle == 1024u) t_prog = globaltimer_ns();
+        } else if ((++idle & 15u) == 0) {   // look at the clock only now and then
+          if (idle == 16u) t_prog = globaltimer_ns();
           if (*s_abort) {
             ok = false;
           } else if (globaltimer_ns() - t_prog > kWaitLimitNs) {
@@ -292,45 +360,11 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       const bool w_ok = mbar_wait(b_, par, s_abort, err);
       return __all_sync(0xffffffffu, w_ok);
     };
-    // V rows of a unit (slot) of the ring: bf16 -> f16 in place; a NaN becomes 0 and a NaN
-    // in the key's K row, at dim 64 (the rotated dims are below it)
-    auto v_unit = [&](int slot) {
-      uint8_t* vb = smem + L::OFF_V + slot * L::UNIT_BYTES;
-      uint4 xv[2];
-#pragma unroll
-      for (int h2 = 0; h2 < 2; ++h2)
-        xv[h2] = *reinterpret_cast<const uint4*>(vb + h2 * L::R_CHUNK + ctid * 16);
-      bool bad = false;
-#pragma unroll
-      for (int h2 = 0; h2 < 2; ++h2) {
-        uint32_t w[4] = {xv[h2].x, xv[h2].y, xv[h2].z, xv[h2].w};
-        bool nan = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
-          nan |= !__hbeq2(x, x);
-        }
-        if (nan) {
-          xv[h2] = make_uint4(0u, 0u, 0u, 0u);
-          bad = true;
-        }
-      }
-      const int row = ctid >> 3;
-      if (bad)
-        *reinterpret_cast<uint16_t*>(smem + L::OFF_K + L::R_CHUNK + slot * L::UNIT_BYTES + row * 128 + ((row & 7) << 4)) = kNan16;
-#pragma unroll
-      for (int h2 = 0; h2 < 2; ++h2)
-        *reinterpret_cast<uint4*>(vb + h2 * L::R_CHUNK + ctid * 16) =
-            make_uint4(bf16x2_to_f16x2(xv[h2].x), bf16x2_to_f16x2(xv[h2].y),
-                       bf16x2_to_f16x2(xv[h2].z), bf16x2_to_f16x2(xv[h2].w));
-    };
     float2 turn[4];   // (cos, sin)(j w_lane) of positions j = warp, warp + 4, .. of a block
     if (half == 32) {
 #pragma unroll
       for (int i2 = 0; i2 < 4; ++i2) {
-        const double ang = static_cast<double>((ctid >> 5) + 4 * i2) * s_invf[lane];
-        const double nrev = rint(ang * 0.15915494309189535);
-        __sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &turn[i2].y, &turn[i2].x);
+        angle((ctid >> 5) + 4 * i2, turn[i2].y, turn[i2].x);
       }
     }
     int seq = 0, i = 0, runs = 0;
@@ -342,13 +376,13 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       const int p0 = p.q_off + t * kSwaP;            // absolute position of the block
       float* tab = reinterpret_cast<float*>(smem + L::OFF_TAB + (i & 1) * L::TAB_BYTES);
       if (ctid == 0) SWA_TRACE(i, 0);
+      // (the softmax warps' units of the first run: landed, and the turns read, before either is touched)
+      if (i == 1 && !wait_all(bar(kSwStart), 0)) break;
       // (cos, sin) of the block's 16 positions (double buffered: tile i - 1 may still read)
       if (half == 32) {
         // one angle per thread (frequency = lane), turned by the four positions the thread serves
-        const double ang = static_cast<double>(p0) * s_invf[lane];
-        const double nrev = rint(ang * 0.15915494309189535);
         float sn, cs;
-        __sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &sn, &cs);
+        angle(p0, sn, cs);
 #pragma unroll
         for (int i2 = 0; i2 < 4; ++i2) {
           float* tk = tab + ((ctid >> 5) + 4 * i2) * 64 + (lane >> 1) * 4 + (lane & 1);
@@ -368,71 +402,45 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         }
       }
       if (half > 0) {
-        mbar_arrive(bar(kSwTab + (i & 1)));   // (bounded waits only: no hardware named barrier)
+        arrive_warp(bar(kSwTab + (i & 1)));   // (bounded waits only: no hardware named barrier)
         if (!wait_all(bar(kSwTab + (i & 1)), (i >> 1) & 1)) break;
+      }
+      // the turns j w_k of a run's start are handed around in the table that the next block will write
+      // (its last reader was the previous block)
+      float* spare = reinterpret_cast<float*>(smem + L::OFF_TAB + ((i + 1) & 1) * L::TAB_BYTES);
+      if (first && half == 32) {
+#pragma unroll
+        for (int i2 = 0; i2 < 4; ++i2) {
+          float* tk = spare + ((ctid >> 5) + 4 * i2) * 64 + (lane >> 1) * 4 + (lane & 1);
+          tk[0] = turn[i2].x;
+          tk[2] = turn[i2].y;
+        }
+        arrive_warp(bar(kSwTurn));
       }
       if (!wait_all(bar(kSwQFull + (i & 1)), (i >> 1) & 1)) break;
       if (ctid == 0) SWA_TRACE(i, 1);
       if (half > 0 && t * kSwaP + (ctid >> 3) < p.n)
         rope_row_tab(smem + L::OFF_Q + (i & 1) * L::Q_STAGE + ctid * 128, ctid, nun,
                      reinterpret_cast<const float4*>(tab + (ctid >> 3) * 64));
-      // K units of this block: the new one, or the whole window at the start of a run
+      // K units of this block: the new one, or at the start of a run the whole window (in the first run
+      // the softmax warps do the eight before the block's own)
       bool ok = true;
-      const int s_first = first ? useq - 8 : useq;
-      for (int s = s_first; s <= useq && ok; ++s) ok = wait_all(bar(kSwKVFull + s % kSwaUnits), (s / kSwaUnits) & 1);
+      const int s_first = first ? useq - 8 : useq, s_mine = i == 0 ? useq : s_first;
+      for (int s = s_mine; s <= useq && ok; ++s) ok = wait_all(bar(kSwKVFull + s % kSwaUnits), (s / kSwaUnits) & 1);
       if (!ok) break;
-      for (int s = s_first; s <= useq; ++s) v_unit(s % kSwaUnits);   // V units entering the ring
+      for (int s = s_mine; s <= useq; ++s) v_part(s % kSwaUnits, ctid);   // V units entering the ring
       if (first) {                                 // and the first tokens' unit of a new run
         if (!wait_all(bar(kSwFirstFull), runs & 1)) break;
-        v_unit(kSwaUnits);
-        if (half == 32) {
-          // K of the window's units and of the first tokens, two units per turn: thread (row, 16-byte
-          // unit) takes the angles of its unit's first position from the lanes (frequency = lane) and
-          // turns them by its row's. The turns j w_k (see `turn`) are handed around in the table that
-          // the next block will write (its last reader was the previous block).
-          float* spare = reinterpret_cast<float*>(smem + L::OFF_TAB + ((i + 1) & 1) * L::TAB_BYTES);
-#pragma unroll
-          for (int i2 = 0; i2 < 4; ++i2) {
-            float* tk = spare + ((ctid >> 5) + 4 * i2) * 64 + (lane >> 1) * 4 + (lane & 1);
-            tk[0] = turn[i2].x;
-            tk[2] = turn[i2].y;
-          }
-          mbar_arrive(bar(kSwTurn));
+        v_part(kSwaUnits, ctid);
+        if (half == 32) {   // K of the window's units and of the first tokens, two units per turn
           if (!wait_all(bar(kSwTurn), runs & 1)) break;
-          const int row = (ctid >> 2) & 15, u = ctid & 3;
-          const float4* t4 = reinterpret_cast<const float4*>(spare + row * 64);
 #pragma unroll 1
-          for (int k2 = ctid >> 6; k2 <= kSwaWin; k2 += 2) {   // 0 .. 8: the window's, 9: the first tokens'
+          for (int k2 = (i == 0 ? 8 : 0) + (ctid >> 6); k2 <= kSwaWin; k2 += 2) {   // 9: the first tokens'
             const bool own = k2 < kSwaWin;
-            const int kpos0 = own ? p0 - 128 + 16 * k2 : 0, kpos = kpos0 + row;
-            const int ring_row = (own ? (s_first + k2) % kSwaUnits : kSwaUnits) * 16 + row;
-            const double ang = static_cast<double>(kpos0) * s_invf[lane];
-            const double nrev = rint(ang * 0.15915494309189535);
+            const int kpos0 = own ? p0 - 128 + 16 * k2 : 0;
             float bs, bc;
-            __sincosf(static_cast<float>(fma(-nrev, 6.283185307179586, ang)), &bs, &bc);
-            const bool raw = kpos >= p.krot_from && kpos < p.nk, cooked = kpos >= 0 && kpos < p.krot_from;
-            uint4* px = reinterpret_cast<uint4*>(smem + L::OFF_K + ring_row * 128 + ((u ^ (row & 7)) << 4));
-            uint4* py = reinterpret_cast<uint4*>(smem + L::OFF_K + ring_row * 128 + (((u + 4) ^ (row & 7)) << 4));
-            const uint4 x = *px, y = *py;
-            uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int e2 = 0; e2 < 4; ++e2) {
-              const int k = u * 8 + 2 * e2;
-              const float4 t = t4[u * 4 + e2];
-              const float c0 = __shfl_sync(0xffffffffu, bc, k), s0 = __shfl_sync(0xffffffffu, bs, k);
-              const float c1 = __shfl_sync(0xffffffffu, bc, k + 1), s1 = __shfl_sync(0xffffffffu, bs, k + 1);
-              if (raw) {
-                rot_pair(xs[e2], ys[e2], make_float4(c0 * t.x - s0 * t.z, c1 * t.y - s1 * t.w,
-                                                     s0 * t.x + c0 * t.z, s1 * t.y + c1 * t.w));
-              } else if (cooked) {
-                xs[e2] = bf16x2_to_f16x2(xs[e2]);
-                ys[e2] = bf16x2_to_f16x2(ys[e2]);
-              }
-            }
-            if (raw || cooked) {
-              *px = make_uint4(xs[0], xs[1], xs[2], xs[3]);
-              *py = make_uint4(ys[0], ys[1], ys[2], ys[3]);
-            }
+            angle(kpos0, bs, bc);
+            k_part(own ? (s_first + k2) % kSwaUnits : kSwaUnits, ctid & 63, kpos0, bc, bs, spare);
           }
         } else if (half > 0 && ctid < 16) {
           const int ring_row = kSwaUnits * 16 + ctid;
@@ -440,14 +448,12 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
           else if (ctid < p.krot_from) f16_row(sK, L::R_CHUNK, ring_row, p.rot_dims);
         }
         ++runs;
-        fence_proxy_async_smem();
-        mbar_arrive(bar(kSwFirstReady));
       }
       if (half > 0) {
         if (first && half == 32) {
           // done above
         } else if (first) {
-          for (int rr = ctid; rr < 16 * kSwaWin; rr += 128) {
+          for (int rr = (i == 0 ? 128 : 0) + ctid; rr < 16 * kSwaWin; rr += 128) {
             const int kpos = p0 - 128 + rr;
             const int ring_row = ((s_first + rr / 16) % kSwaUnits) * 16 + (rr & 15);
             if (kpos >= p.krot_from && kpos < p.nk) rope_row(sK, L::R_CHUNK, ring_row, kpos, p.rot_dims, s_invf);
@@ -462,8 +468,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(bar(kSwQReady + (i & 1)));
-      for (int s = s_first; s <= useq; ++s) mbar_arrive(bar(kSwKReady + s % kSwaUnits));
+      arrive_warp(bar(kSwQReady + (i & 1)));
       if (lane == 0) SWA_TRACE(i, 21 + (ctid >> 5));
     }
   } else {
@@ -478,8 +483,32 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       const bool w_ok = mbar_wait(b_, par, s_abort, err);
       return __all_sync(0xffffffffu, w_ok);
     };
+    // the first run's unit that this warp asked for (the RoPE group alone took 5500 cycles for all ten of
+    // a run's start, a third of a short call)
+    bool started = true;
+    {
+      const int slot = warp - 6, kpos0 = p.q_off + static_cast<int>(f0 % nqt) * kSwaP - 128 + 16 * slot;
+      float bs = 0.f, bc = 0.f;
+      if (half == 32) angle(kpos0, bs, bc);
+      started = wait_all(bar(kSwKVFull + slot), 0) && (half != 32 || wait_all(bar(kSwTurn), 0));
+      if (started) {
+#pragma unroll 1
+        for (int x = lane; x < 128; x += 32) v_part(slot, x);
+        const float* turns = reinterpret_cast<const float*>(smem + L::OFF_TAB + L::TAB_BYTES);
+        if (half == 32) {
+#pragma unroll 1
+          for (int x = lane; x < 64; x += 32) k_part(slot, x, kpos0, bc, bs, turns);
+        } else if (half > 0 && lane < 16) {
+          const int kpos = kpos0 + lane;
+          if (kpos >= p.krot_from && kpos < p.nk) rope_row(sK, L::R_CHUNK, slot * 16 + lane, kpos, p.rot_dims, s_invf);
+          else if (kpos >= 0 && kpos < p.krot_from) f16_row(sK, L::R_CHUNK, slot * 16 + lane, p.rot_dims);
+        }
+        fence_proxy_async_smem();
+        arrive_warp(bar(kSwStart));
+      }
+    }
     int seq = 0, i = 0;
-    for (long long f = f0; f < f1; ++f, ++i) {
+    for (long long f = f0; f < f1 && started; ++f, ++i) {
       const int bg = static_cast<int>(f / nqt), t = static_cast<int>(f % nqt);
       const bool first = (f == f0 || t == 0);
       if (first) seq += 8;
@@ -600,7 +629,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       ref = ref == -INFINITY ? 0.f : ref;                 // a row without keys
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(bar(kSwPReady + w));
+      arrive_warp(bar(kSwPReady + w));
       if (lane == 0) SWA_TRACE(i, 25 + (ctid >> 5));
       const float sum = sum0 + sum1;
       // denominator with the sink: M = max(amax, sink); l = sum 2^(amax-M) + 2^(sink-M)
@@ -625,7 +654,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         tmem_wait_ld();
         if (hh == 1) {
           tc_fence_before();
-          mbar_arrive(bar(kSwTmFree + w));
+          arrive_warp(bar(kSwTmFree + w));
         }
         if (row_ok) {
           const unsigned long long il2 = f2_pack(inv_l, inv_l);
