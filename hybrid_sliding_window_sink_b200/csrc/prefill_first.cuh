@@ -18,7 +18,7 @@
 //     the issuer, took 2000 cycles.
 //   * Every tile masks keys, so a V row that holds a NaN becomes zeros and its K row a NaN as it enters
 //     (see v_row_not_finite in prefill.cuh; infinities are clamped).
-// Bound: bytes at n = 32768 (1.51 GB, 231 us at the measured copy rate); measured 405 us cold, 460 us under
+// Bound: bytes at n = 32768 (1.51 GB, 231 us at the measured copy rate); measured 390 us cold, 445 us under
 // the power cap (the kernel without first tokens 448 and 500). A trace puts the RoPE group and the two
 // softmax groups level at 6200 - 6500 cycles per row block, against 4000 at the byte floor.
 #pragma once
@@ -643,7 +643,8 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       if (ctid == 0) SWA_TRACE(i, 5);
       const bool none = lt == 0.f;                   // no key and no sink (a NaN stays one)
       const float inv_l = none ? 0.f : sc / lt;
-      __nv_bfloat16* orow = p.out + ((static_cast<long long>(b) * p.n + qi) * p.Hq + hq) * 128;
+      const bool odd = lane & 1;                     // (rows of two lanes: heads of one position)
+      __nv_bfloat16* opair = p.out + ((static_cast<long long>(b) * p.n + qi) * p.Hq + (hq & ~1)) * 128 + (odd ? 8 : 0);
       // O columns [128, 192) overlap the S columns of this group's next tile: read them
       // first, release the TMEM region, then finish with columns [192, 256)
 #pragma unroll 1
@@ -656,19 +657,26 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
           tc_fence_before();
           arrive_warp(bar(kSwTmFree + w));
         }
-        if (row_ok) {
-          const unsigned long long il2 = f2_pack(inv_l, inv_l);
+        const unsigned long long il2 = f2_pack(inv_l, inv_l);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t pk[8];
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 o = f2_unpack(f2_mul(f2_bits(v[q][2 * e], v[q][2 * e + 1]), il2));
-              pk[e] = pack_bf16(o.x, o.y);
-            }
-            uint4* dst = reinterpret_cast<uint4*>(orow + (2 * hh + q) * 16);
-            dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          for (int e = 0; e < 8; ++e) {
+            const float2 o = f2_unpack(f2_mul(f2_bits(v[q][2 * e], v[q][2 * e + 1]), il2));
+            pk[e] = pack_bf16(o.x, o.y);
+          }
+          // two lanes write the 32 bytes of the even lane's row, then those of the odd lane's: whole
+          // sectors (n = 32768: 410 us with halves of them, 390 so)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? pk[e] : pk[4 + e], 1);
+            if (odd) pk[e] = got;
+            else pk[4 + e] = got;
+          }
+          if (row_ok) {
+            *reinterpret_cast<uint4*>(opair + (2 * hh + q) * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<uint4*>(opair + 128 + (2 * hh + q) * 16) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
           }
         }
       }
