@@ -211,3 +211,12 @@ def test_scores_that_rise_along_the_window(cuda_device):
         inp["q"][..., 64] = 20.0
         for window, first in ((128, 4), (160, 30)):
             _check(inp, cuda_device, window, first, rot=64, what=f"ramp {sign}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rot", [0, 32, 64])
+@pytest.mark.parametrize("n,off", [(12, 0), (20, 0), (40, 32), (60, 0)])
+def test_runs_over_many_short_sequences(cuda_device, n, off, rot):
+    """More row blocks than SMs, one to four per (sequence, KV head): a CTA's run starts anew at its
+    second block, at its third, and in between."""
+    _check(_inputs(40, n, off, 64, 8, n + rot), cuda_device, 9, 4, off=off, rotated=off > 0, rot=rot, what=f"{n} {off} {rot}")
