@@ -367,16 +367,29 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         angle((ctid >> 5) + 4 * i2, turn[i2].y, turn[i2].x);
       }
     }
+    // Two tables. Block i writes its angles into table i & 1 and, if it begins a run, the run's turns
+    // into the other one, the spare table. Who has read a table before it is written again:
+    //   angles of block i over those of block i - 2: all four warps arrived at kSwTab of block i - 1
+    //     (waited for there), each behind its last read of block i - 2;
+    //   turns of block i over the angles of block i - 1: all four arrived at kSwTab of block i;
+    //   angles of block i + 1 over the turns of block i: kSwQReady of block i, one arrival per warp of this
+    //     group behind its last read of the turns. It is waited for at the head of block i + 1 only where
+    //     block i began a run, and cannot be overtaken there: its next phase is that of block i + 2;
+    //   the same over the turns of the first run, which the softmax warps read too: kSwStart.
     int seq = 0, i = 0, runs = 0;
+    bool turned = false;                             // the previous block left turns in the spare table
     for (long long f = f0; f < f1; ++f, ++i) {
       const int t = static_cast<int>(f % nqt);
       const bool first = (f == f0 || t == 0);
       if (first) seq += 8;
       const int useq = seq++;
       const int p0 = p.q_off + t * kSwaP;            // absolute position of the block
+      if (turned && !wait_all(bar(kSwQReady + ((i - 1) & 1)), ((i - 1) >> 1) & 1)) break;
+      turned = first && half == 32;
       float* tab = reinterpret_cast<float*>(smem + L::OFF_TAB + (i & 1) * L::TAB_BYTES);
       if (ctid == 0) SWA_TRACE(i, 0);
-      // (the softmax warps' units of the first run: landed, and the turns read, before either is touched)
+      // (the softmax warps' units of the first run: landed, and the turns read, before either is touched:
+      // see the tables above)
       if (i == 1 && !wait_all(bar(kSwStart), 0)) break;
       // (cos, sin) of the block's 16 positions (double buffered: tile i - 1 may still read)
       if (half == 32) {
@@ -406,7 +419,6 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         if (!wait_all(bar(kSwTab + (i & 1)), (i >> 1) & 1)) break;
       }
       // the turns j w_k of a run's start are handed around in the table that the next block will write
-      // (its last reader was the previous block)
       float* spare = reinterpret_cast<float*>(smem + L::OFF_TAB + ((i + 1) & 1) * L::TAB_BYTES);
       if (first && half == 32) {
 #pragma unroll

@@ -220,3 +220,15 @@ def test_runs_over_many_short_sequences(cuda_device, n, off, rot):
     """More row blocks than SMs, one to four per (sequence, KV head): a CTA's run starts anew at its
     second block, at its third, and in between."""
     _check(_inputs(40, n, off, 64, 8, n + rot), cuda_device, 9, 4, off=off, rotated=off > 0, rot=rot, what=f"{n} {off} {rot}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [20, 36, 60])
+def test_run_starts_repeat_bit_for_bit(cuda_device, n):
+    """Several run starts per CTA (two to four row blocks per (sequence, KV head)), each followed by a
+    block that writes the table which held the start's turns: the same bits every time."""
+    inp = {k: v.to(cuda_device) for k, v in _inputs(60, n, 0, 64, 8, 90 + n).items()}
+    want = _lib.prefill_first(inp["q"], inp["k"], inp["v"], inp["sink"], window=11, n_first=4)
+    for _ in range(60):
+        got = _lib.prefill_first(inp["q"], inp["k"], inp["v"], inp["sink"], window=11, n_first=4)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
