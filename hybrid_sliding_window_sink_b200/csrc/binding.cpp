@@ -99,7 +99,11 @@ struct Args {
     }
     return static_cast<float>(v);
   }
-  bool flag(int i) const { return a[i] == Py_True; }
+  // True or False itself; _lib.py goes by the truth value of anything else
+  bool flag(int i) {
+    if (a[i] != Py_True && a[i] != Py_False) ok = false;
+    return a[i] == Py_True;
+  }
   static void* data(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
 };
 
@@ -182,6 +186,7 @@ PyObject* decode_paged(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (in.given(7)) sink = in.tensor(7, at::kFloat, {hq});
     const int window = in.integer(8), first = in.integer(9);
     const float scale = in.real(10);
+    const bool want_lse = in.flag(11);
     long long stride = -1;
     if (!in.ok || !pool(*k, stride) || !pool(*v, stride) || (fp8 && (!pool(*ks, stride) || !pool(*vs, stride))))
       Py_RETURN_NONE;
@@ -190,7 +195,7 @@ PyObject* decode_paged(PyObject*, PyObject* const* args, Py_ssize_t n) {
                            static_cast<int>(N), static_cast<int>(page), stride};
     const size_t bytes = fn.workspace_size(&shape, &pages, window, first);
     at::Tensor out = fresh({B, hq, 128}, at::kBFloat16, *q), lse;
-    if (in.flag(11)) lse = fresh({B, hq}, at::kFloat, *q);
+    if (want_lse) lse = fresh({B, hq}, at::kFloat, *q);
     c10::DataPtr ws;                       // (goes back to the allocator in stream order)
     if (bytes) ws = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
     void* st = c10::cuda::getCurrentCUDAStream().stream();
@@ -263,7 +268,8 @@ PyObject* prefill_first(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args in{args};
     const at::Tensor* q = in.tensor(0, at::kBFloat16, {-1, -1, -1, 192});
     const int off = in.integer(6);
-    if (!in.ok || off < 0 || (args[7] != Py_True && args[7] != Py_False)) Py_RETURN_NONE;
+    const bool rotated = in.flag(7), want_lse = in.flag(11);
+    if (!in.ok || off < 0) Py_RETURN_NONE;
     const int64_t B = q->size(0), len = q->size(1), hq = q->size(2);
     const at::Tensor* k = in.tensor(1, at::kBFloat16, {B, off + len, -1, 192});
     if (!in.ok) Py_RETURN_NONE;
@@ -276,9 +282,9 @@ PyObject* prefill_first(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const mimo_shape shape{static_cast<int>(B), static_cast<int>(len), static_cast<int>(hq), static_cast<int>(hkv), 192,
                            128, scale};
     at::Tensor out = fresh({B, len, hq, 128}, at::kBFloat16, *q), lse;
-    if (in.flag(11)) lse = fresh({B, hq, len}, at::kFloat, *q);
+    if (want_lse) lse = fresh({B, hq, len}, at::kFloat, *q);
     const mimo_status rc = fn.prefill_first(
-        &shape, q->data_ptr(), k->data_ptr(), v->data_ptr(), off, in.flag(7), static_cast<float*>(Args::data(sink)),
+        &shape, q->data_ptr(), k->data_ptr(), v->data_ptr(), off, rotated, static_cast<float*>(Args::data(sink)),
         window, first, theta, rot, out.data_ptr(), lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
         c10::cuda::getCurrentCUDAStream().stream());
     if (rc != MIMO_OK) Py_RETURN_NONE;

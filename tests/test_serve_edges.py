@@ -139,3 +139,19 @@ def test_verify_rows_at_any_alignment(cuda_device, V, shift, dtype):
         want = serve.verify_drafts(wl.to_f64(p.cpu()), None if given is None else wl.to_f64(q.cpu()),
                                    draft.numpy(), wl.to_f64(u))
         assert acc.tolist() == want[0].tolist() and tok.tolist() == want[1].tolist()
+
+
+def test_want_lse_goes_by_its_truth_value(cuda_device, monkeypatch):
+    """Both marshallings, with everything that is not a bool itself."""
+    d = to_dev(paged_inputs([40, 20], 8, 1, 16, seed=8), cuda_device)
+    x = {k: v.to(cuda_device) for k, v in wl.prefill_inputs(1, 40, 8, 1, seed=9).items()}
+    calls = [lambda w: _lib.decode_paged(d["q"], d["k"], d["v"], d["table"], d["lengths"], want_lse=w),
+             lambda w: _lib.prefill_first(x["q"], x["k"], x["v"], window=30, n_first=5, want_lse=w)]
+    for usual in (_lib._usual, lambda: False):
+        monkeypatch.setattr(_lib, "_usual", usual)
+        for call in calls:
+            want = call(True)[1]
+            for yes in (1, np.bool_(True), "yes", [0]):
+                assert torch.equal(call(yes)[1], want), yes
+            for no in (False, 0, np.bool_(False), None, ""):
+                assert call(no)[1] is None, no
