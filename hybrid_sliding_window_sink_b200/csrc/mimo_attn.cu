@@ -332,12 +332,13 @@ mimo_status prefill_chunk_group(const mimo_shape* s, const void* q, const void* 
 
 // A window with the first n_first tokens kept visible: the ring kernel where its window and
 // first tokens fit (its row blocks read each key once per run), the pair kernel for the other
-// windows of 8 and 16 heads per KV head, the generic kernel for the rest.
+// windows of 8 and 16 heads per KV head, the generic kernel for the rest. A window that holds every key
+// takes the kernel that a causal prefix takes, the pair kernel or the generic one.
 template <int G>
 mimo_status prefill_first_group(const mimo_shape* s, const void* q, const void* k, const void* v,
                                 const PrefillFirstParams& prm, int sms, cudaStream_t st) {
-  if (G == mimo::kSwaG && prm.window <= 129 && prm.n_first <= mimo::kSwaFirst && prm.rot_dims <= 64 &&
-      prm.q_off % mimo::kSwaP == 0)
+  if (G == mimo::kSwaG && prm.window < prm.nk && prm.window <= 129 && prm.n_first <= mimo::kSwaFirst &&
+      prm.rot_dims <= 64 && prm.q_off % mimo::kSwaP == 0)
     return launch_prefill_swa<true>(s, q, k, v, prm, sms, st);
   if constexpr (G == 8 || G == 16) {
     if (prm.rot_dims <= 64) return launch_prefill_ga<G, true>(s, q, k, v, prm, sms, st);
@@ -760,8 +761,10 @@ mimo_status run_prefill_chunk(const mimo_shape* s, const void* q, const void* k,
   const int sms = sm_count_for(dev);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int group = s->n_q_heads / s->n_kv_heads;
-  // without a window that ends inside the keys, the first tokens are visible anyway
-  if (n_first > 0 && window > 0 && window < prm.nk) {
+  // A window that holds every key (the first tokens among them) takes the same kernels: they keep V rows
+  // that are not finite away from the queries that mask them, as the padding of a short batch may hold.
+  if (n_first > 0 && window > 0) {
+    prm.window = std::min(window, prm.nk);   // (the kernels subtract it from positions in 32 bits)
     inv_freqs(prm.rope_theta, rot_dims, prm.invf);
     switch (group) {
       case 1: return prefill_first_group<1>(s, q, k, v, prm, sms, st);

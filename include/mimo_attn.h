@@ -309,13 +309,13 @@ size_t mimo_attn_select_workspace_size(const mimo_shape* shape, int cache_capaci
  * Prefill with a sliding window and pinned first tokens: as mimo_attn_prefill_chunk (whole
  * sequences with pos_offset = 0), but the query at position i sees
  *   J_i = [max(0, i - window + 1), i] and [0, n_first)
- * (a token in both counts once). n_first >= 0, any size; n_first = 0, window <= 0 or window >=
- * pos_offset + n is mimo_attn_prefill_chunk itself. Positions stay absolute: a first token keeps
- * its own rotation. Errors as mimo_attn_prefill_chunk, MIMO_ERR_SHAPE also for n_first < 0.
+ * (a token in both counts once). n_first >= 0, any size; n_first = 0 or window <= 0 is
+ * mimo_attn_prefill_chunk itself. Positions stay absolute: a first token keeps its own rotation.
+ * Errors as mimo_attn_prefill_chunk, MIMO_ERR_SHAPE also for n_first < 0.
  * The decode of such a layer is mimo_attn_decode_paged with the same window and n_first.
- * A V row that is not finite does not reach queries that mask its key (behind them in a padded
- * batch, say); queries that see a NaN in a V row become NaN, all 128 columns where the key's tile is
- * masked in part.
+ * With window > 0 and n_first > 0, a V row that is not finite does not reach queries that mask its key
+ * (behind them in a padded batch, say); queries that see a NaN in a V row become NaN, all 128 columns
+ * where the key's tile is masked in part.
  */
 mimo_status mimo_attn_prefill_first(const mimo_shape* shape, const void* q, const void* k, const void* v,
                                     int pos_offset, int k_prefix_rotated, const float* sink, int window,

@@ -232,3 +232,29 @@ def test_run_starts_repeat_bit_for_bit(cuda_device, n):
     for _ in range(60):
         got = _lib.prefill_first(inp["q"], inp["k"], inp["v"], inp["sink"], window=11, n_first=4)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,rot", [(8, 1, 64), (16, 1, 64), (4, 2, 64), (8, 1, 128)])
+@pytest.mark.parametrize("n,off", [(100, 0), (75, 16), (300, 0)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_padding_of_a_batch_shorter_than_its_window(cuda_device, hq, hkv, rot, n, off, bad):
+    """Rows behind a sequence's end that are not finite, where the window holds every key (n below the
+    default window among them): the queries before them mask them and stay what they are."""
+    end = n - 20
+    window = max(128, off + n)
+    inp = _inputs(2, n, off, hq, hkv, 95 + n)
+    clean = {k: v.clone() for k, v in inp.items()}
+    inp["k"][1, off + end:] = bad
+    inp["v"][1, off + end:] = bad
+    clean["v"][1, off + end:] = 0
+    clean["k"][1, off + end:] = 0
+    d = {k: v.to(cuda_device) for k, v in inp.items()}
+    out, lse = _lib.prefill_first(d["q"], d["k"], d["v"], d["sink"], window=window, n_first=4, pos_offset=off,
+                                  k_prefix_rotated=False, rot_dims=rot)
+    torch.cuda.synchronize()
+    o, l, mass = serve.prefill_first(*(wl.to_f64(clean[x]) for x in "qkv"), off, False, wl.to_f64(inp["sink"]), window, 4,
+                                     1e4, rot)
+    check(out[:, :end].contiguous(), lse[:, :, :end], o[:, :end], l[:, :, :end], mass[:, :end], BF16, _delta(clean, rot),
+          f"{hq}/{hkv} n {n}")
+    check(out[:1], lse[:1], o[:1], l[:1], mass[:1], BF16, _delta(clean, rot), "the sequence without padding")
