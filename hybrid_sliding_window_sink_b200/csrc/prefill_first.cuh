@@ -16,8 +16,8 @@
 //   * K has no barrier of its own (Q of a block is handed over after the block's K and V), and a group
 //     hands over by one arrival per warp: a thousand arrivals at a run's start, and the nine polls of
 //     the issuer, took 2000 cycles.
-//   * Every tile masks keys, so a V row that holds a NaN becomes zeros and its K row a NaN as it enters
-//     (see v_row_not_finite in prefill.cuh; infinities are clamped).
+//   * Every tile masks keys, so in a V row that holds a NaN or an infinity the 16 bytes around it become
+//     zeros and its K row a NaN as it enters (see v_row_not_finite in prefill.cuh).
 // Bound: bytes at n = 32768 (1.51 GB, 231 us at the measured copy rate); measured 390 us cold, 445 us under
 // the power cap (the kernel without first tokens 448 and 500). A trace puts the RoPE group and the two
 // softmax groups level at 6200 - 6500 cycles per row block, against 4000 at the byte floor.
@@ -133,8 +133,9 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(b_);
   };
-  // V, sixteen bytes of each half of row x / 8 of a unit (slot) of the ring: bf16 -> f16 in place; a NaN
-  // becomes 0 and a NaN in the key's K row, at dim 64 (the rotated dims are below it)
+  // V, sixteen bytes of each half of row x / 8 of a unit (slot) of the ring: bf16 -> f16 in place; sixteen
+  // bytes with a value that is not finite become zeros, and dim 64 of the key's K row a NaN (the rotated dims
+  // are below it)
   auto v_part = [&](int slot, int x) {
     uint8_t* vb = smem + L::OFF_V + slot * L::UNIT_BYTES;
     uint4 xv[2];
@@ -142,16 +143,14 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
     for (int h2 = 0; h2 < 2; ++h2)
       xv[h2] = *reinterpret_cast<const uint4*>(vb + h2 * L::R_CHUNK + x * 16);
     bool bad = false;
+    const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
 #pragma unroll
     for (int h2 = 0; h2 < 2; ++h2) {
-      uint32_t w[4] = {xv[h2].x, xv[h2].y, xv[h2].z, xv[h2].w};
-      bool nan = false;
+      const uint32_t w[4] = {xv[h2].x, xv[h2].y, xv[h2].z, xv[h2].w};
+      __nv_bfloat162 acc = zero;                     // 0, or a NaN (see v_row_not_finite)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 x2 = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
-        nan |= !__hbeq2(x2, x2);
-      }
-      if (nan) {
+      for (int e = 0; e < 4; ++e) acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), zero, acc);
+      if (!__hbeq2(acc, zero)) {
         xv[h2] = make_uint4(0u, 0u, 0u, 0u);
         bad = true;
       }

@@ -314,8 +314,9 @@ size_t mimo_attn_select_workspace_size(const mimo_shape* shape, int cache_capaci
  * Errors as mimo_attn_prefill_chunk, MIMO_ERR_SHAPE also for n_first < 0.
  * The decode of such a layer is mimo_attn_decode_paged with the same window and n_first.
  * With window > 0 and n_first > 0, a V row that is not finite does not reach queries that mask its key
- * (behind them in a padded batch, say); queries that see a NaN in a V row become NaN, all 128 columns
- * where the key's tile is masked in part.
+ * (behind them in a padded batch, say). A query that sees it is not finite in the columns of V's NaN and
+ * infinities; where some query of the same tile masks the key (everywhere with window <= 129, 8 heads per KV
+ * head) all its 128 columns and its lse become NaN, although lse does not depend on V.
  */
 mimo_status mimo_attn_prefill_first(const mimo_shape* shape, const void* q, const void* k, const void* v,
                                     int pos_offset, int k_prefix_rotated, const float* sink, int window,

@@ -258,3 +258,24 @@ def test_padding_of_a_batch_shorter_than_its_window(cuda_device, hq, hkv, rot, n
     check(out[:, :end].contiguous(), lse[:, :, :end], o[:, :end], l[:, :, :end], mass[:, :end], BF16, _delta(clean, rot),
           f"{hq}/{hkv} n {n}")
     check(out[:1], lse[:1], o[:1], l[:1], mass[:1], BF16, _delta(clean, rot), "the sequence without padding")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,window,first", [(8, 1, 128, 4), (8, 1, 200, 40), (16, 1, 64, 130), (4, 2, 128, 4),
+                                                 (4, 2, 400, 4), (2, 2, 300, 140), (8, 1, 400, 1)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite_show_where_they_are_seen(cuda_device, hq, hkv, window, first, bad):
+    """A query that sees a V row with a NaN or an infinity is not finite in that column, in every kernel."""
+    n, at = 400, [2, 150, 333]
+    inp = _inputs(1, n, 0, hq, hkv, 73)
+    for t in at:
+        inp["v"][0, t, 0, t % 128] = bad
+    d = {k: v.to(cuda_device) for k, v in inp.items()}
+    out, _ = _lib.prefill_first(d["q"], d["k"], d["v"], d["sink"], window=window, n_first=first)
+    torch.cuda.synchronize()
+    for t in at:
+        sees = [i for i in range(t, n) if t > i - window or t < first]
+        assert not torch.isfinite(out[0, sees, :hq // hkv, t % 128]).any(), t
+        hides = [i for i in range(n) if not any(u <= i and (u > i - window or u < first) for u in at)]
+        assert torch.isfinite(out[0, hides]).all()
+    assert torch.isfinite(out[0, :, hq // hkv:]).all()
