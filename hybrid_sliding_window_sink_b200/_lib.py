@@ -496,6 +496,14 @@ def _need_at(t, name, dtype, shape, device, contiguous=True):
     raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
+def _int(x, name):
+    """x as an int that the C ABI can take (ctypes would drop its upper bits)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} = {x} does not fit in 32 bits")
+    return x
+
+
 @functools.lru_cache(maxsize=1024)
 def _fits(have, shape):
     return len(have) == len(shape) and all(n is None or n == h for n, h in zip(shape, have))
@@ -519,7 +527,8 @@ def prefill_first(q, k, v, sink=None, *, window, n_first, pos_offset=0, k_prefix
                                  softmax_scale, want_lse)
         if got is not None:
             return got
-    window, n_first, pos_offset, rot_dims = int(window), int(n_first), int(pos_offset), int(rot_dims)
+    window, n_first = _int(window, "window"), _int(n_first, "n_first")
+    pos_offset, rot_dims = _int(pos_offset, "pos_offset"), _int(rot_dims, "rot_dims")
     rope_theta, softmax_scale = float(rope_theta), float(softmax_scale)
     dev = _cuda_device(q, "q")
     _need_at(q, "q", torch.bfloat16, (None, None, None, 192), dev)
@@ -583,7 +592,8 @@ def _pages(k, v, table, scales=None):
     else:
         a, b = scales
         stride = _pools_stride(ks, k.stride(), v.shape, v.stride(), a.shape, a.stride(), b.shape, b.stride())
-    return MimoPages(table.data_ptr(), table.shape[1], ks[0], ks[1], stride)
+    return MimoPages(table.data_ptr(), _int(table.shape[1], "max_pages"), _int(ks[0], "num_pages"),
+                     _int(ks[1], "page_size"), stride)
 
 
 def _need_pools(k, v, scales, hkv, dev):
@@ -600,6 +610,8 @@ def _need_pools(k, v, scales, hkv, dev):
 @functools.lru_cache(maxsize=1024)
 def _shape_struct(batch, seqlen, hq, hkv, softmax_scale):
     """mimo_shape of these sizes (only ever read)."""
+    for x, name in ((batch, "batch"), (seqlen, "tokens"), (hq, "query heads"), (hkv, "KV heads")):
+        _int(x, name)
     return MimoShape(batch, seqlen, hq, hkv, 192, 128, softmax_scale)
 
 
@@ -617,7 +629,7 @@ def _decode_paged(q, k, v, scales, table, lengths, sink, window, n_first, softma
         got = call.decode_paged(q, k, v, ks, vs, table, lengths, sink, window, n_first, softmax_scale, want_lse)
         if got is not None:
             return got
-    window, n_first, softmax_scale = int(window), int(n_first), float(softmax_scale)
+    window, n_first, softmax_scale = _int(window, "window"), _int(n_first, "n_first"), float(softmax_scale)
     dev = _cuda_device(q, "q")
     _need_at(q, "q", torch.bfloat16, (None, None, 192), dev)
     B, hq, _ = q.shape
@@ -678,8 +690,9 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, lengths
 
 def decode_paged_workspace_size(batch, hq, hkv, *, max_pages, page_size, window=0, n_first=0):
     """Bytes of workspace the paged decodes need on the current device."""
-    return _paged_workspace(torch.cuda.current_device(), int(batch), int(hq), int(hkv), int(max_pages), int(page_size),
-                            int(window), int(n_first))
+    return _paged_workspace(torch.cuda.current_device(), _int(batch, "batch"), _int(hq, "hq"), _int(hkv, "hkv"),
+                            _int(max_pages, "max_pages"), _int(page_size, "page_size"), _int(window, "window"),
+                            _int(n_first, "n_first"))
 
 
 def _append_paged(k_new, v_new, k, v, scales, table, positions, n_new, rope_theta, rot_dims, stream):
@@ -687,7 +700,7 @@ def _append_paged(k_new, v_new, k, v, scales, table, positions, n_new, rope_thet
         ks, vs = (None, None) if scales is None else scales
         if call.append_paged(k_new, v_new, k, v, ks, vs, table, positions, n_new, rope_theta, rot_dims):
             return
-    rope_theta, rot_dims = float(rope_theta), int(rot_dims)
+    rope_theta, rot_dims = float(rope_theta), _int(rot_dims, "rot_dims")
     dev = _cuda_device(k_new, "k_new")
     _need_at(k_new, "k_new", torch.bfloat16, (None, None, None, 192), dev)
     B, n, hkv, _ = k_new.shape
@@ -751,6 +764,8 @@ def verify_drafts(target_probs, draft_tokens, uniforms, draft_probs=None, *, n_v
     T = T1 - 1
     if T < 0:
         raise ValueError("target_probs must have T + 1 rows per sequence")
+    for x, name in ((B, "batch"), (T, "drafts"), (V, "vocabulary")):
+        _int(x, name)
     _need_at(draft_tokens, "draft_tokens", torch.int32, (B, T), dev)
     _need_at(uniforms, "uniforms", torch.float32, (B, T1), dev)
     if draft_probs is not None:

@@ -155,3 +155,35 @@ def test_want_lse_goes_by_its_truth_value(cuda_device, monkeypatch):
                 assert torch.equal(call(yes)[1], want), yes
             for no in (False, 0, np.bool_(False), None, ""):
                 assert call(no)[1] is None, no
+
+
+@pytest.mark.parametrize("usual", [True, False])
+def test_numbers_beyond_32_bits_are_refused(cuda_device, monkeypatch, usual):
+    """The C ABI counts in 32 bits: a window of 2^32 + 5 is not one of 5."""
+    if not usual:
+        monkeypatch.setattr(_lib, "_usual", lambda: False)
+    d = to_dev(paged_inputs([40, 20], 8, 1, 16, seed=8), cuda_device)
+    args = [d[x] for x in ("q", "k", "v", "table", "lengths")]
+    x = {k: v.to(cuda_device) for k, v in wl.prefill_inputs(1, 40, 8, 1, seed=9).items()}
+    qkv = [x[k] for k in "qkv"]
+    kn, vn = (torch.zeros(2, 1, 1, w, dtype=torch.bfloat16, device=cuda_device) for w in (192, 128))
+    for big in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1, 2 ** 70):
+        for kw in (dict(window=big), dict(window=5, n_first=big)):
+            with pytest.raises(ValueError, match="32 bits"):
+                _lib.decode_paged(*args, **kw)
+            with pytest.raises(ValueError, match="32 bits"):
+                _lib.prefill_first(*qkv, **{"n_first": 1, **kw})
+            with pytest.raises(ValueError, match="32 bits"):
+                _lib.decode_paged_workspace_size(2, 8, 1, max_pages=3, page_size=16, **kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            _lib.prefill_first(*qkv, window=5, n_first=1, rot_dims=big)
+        with pytest.raises(ValueError):
+            _lib.prefill_first(*qkv, window=5, n_first=1, pos_offset=big)
+        with pytest.raises(ValueError, match="32 bits"):
+            _lib.cache_append_paged(kn, vn, d["k"], d["v"], d["table"], d["lengths"], rot_dims=big)
+        with pytest.raises(ValueError, match="32 bits"):
+            _lib.decode_paged_workspace_size(2, 8, 1, max_pages=big, page_size=16)
+    V = 2 ** 32 + 3                                      # 8 GB a row, never touched
+    p = torch.empty(1, 1, V, dtype=torch.bfloat16, device=cuda_device)
+    with pytest.raises(ValueError, match="32 bits"):
+        _lib.verify_drafts(p, torch.empty(1, 0, dtype=torch.int32, device=cuda_device), torch.zeros(1, 1, device=cuda_device))
