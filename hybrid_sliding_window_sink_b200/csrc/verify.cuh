@@ -90,9 +90,11 @@ struct VfVec<__nv_bfloat16> {
 };
 
 // A running sum of weights as two floats, s + c: the difference p - q (error e) and the addition
-// to s (its error) are split exactly, and c collects the errors. A lane adds some 100 weights, so
-// the sum is good to about 2^-43 of itself, where a token weighs 2^-17; converting every value to
-// double instead made the kernel 2.5 times slower (the conversions, at V = 131072).
+// to s (its error) are split exactly, and c collects the errors. c itself rounds: after N weights it is at
+// most N 2^-24 of the sum, so off by at most N^2 2^-48 of it, and in steps of random sign by about
+// N 2^-50. At N <= 256 (kVfSpan) that is 2^-32 at the very worst and 2^-42 as a rule, where a token
+// weighs 2^-17; converting every value to double instead made the kernel 2.5 times slower (the
+// conversions, at V = 131072).
 struct VfSum {
   float s = 0.f, c = 0.f;
   __device__ __forceinline__ void add(float p, float q) {
@@ -198,6 +200,10 @@ __device__ __forceinline__ double vf_piece(const E* p, const E* q, int hot, int 
   return sum[0].get() + sum[1].get();
 }
 
+// Values that a warp adds before its lanes' sums move into doubles: 256 a lane and sum. Only rows beyond
+// 2^20 have longer pieces (without this a row of equal weights, V = 2^27, drifted by a token).
+constexpr int kVfSpan = 2 * 32 * 256;
+
 static_assert(kVfMaxCluster * kVfWarps <= 64, "two pieces a lane");
 
 template <typename E, bool VEC>
@@ -252,7 +258,9 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
   for (;;) {
     const long long v0 = static_cast<long long>(mine) * prm.piece;
     double sum = 0.0;
-    if (v0 < V) sum = vf_piece<E, VEC>(p, q, hot, static_cast<int>(v0), static_cast<int>(min(v0 + prm.piece, static_cast<long long>(V))));
+    const int v1 = static_cast<int>(min(v0 + prm.piece, static_cast<long long>(V)));
+    for (long long at = v0; at < v1; at += kVfSpan)
+      sum += vf_piece<E, VEC>(p, q, hot, static_cast<int>(at), static_cast<int>(min(at + kVfSpan, static_cast<long long>(v1))));
     sum = vf_warp_sum(sum);
     if (!started) cluster.barrier_wait();
     started = true;

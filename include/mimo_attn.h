@@ -419,7 +419,8 @@ enum { MIMO_PROBS_F32 = 0, MIMO_PROBS_BF16 = 1 };
  *   next token = the smallest v with w(0) + .. + w(v) > u[T] * (sum of w).
  * The rows need not sum to 1 (but to less than 2^127). Negative and non-finite weights count as 0.
  * Where nothing is left of p_a - q_a, p_a itself is sampled; a target row without mass gives the
- * token -1. u q < p is decided exactly; running sums are good to about 2^-43 of the total.
+ * token -1. u q < p is decided exactly; running sums are good to about 2^-42 of the total (2^-32 at the
+ * worst), for every vocab.
  *
  *  target_probs [B, T + 1, V] device; row t is the target's distribution of the token after t
  *               accepted drafts. fp32 or bf16 (probs_type); V <= 2^30

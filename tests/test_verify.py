@@ -136,3 +136,20 @@ def test_streams_graph_and_buffers(cuda_device):
         want = _lib.verify_drafts(c["p"], c["draft"], c["u"], c["q"])
         torch.cuda.synchronize()
         assert torch.equal(acc, want[0]) and torch.equal(tok, want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 2 ** 27), (torch.float32, 2 ** 27 - 3), (torch.bfloat16, 2 ** 27),
+                                     (torch.bfloat16, 2 ** 27 - 3)])
+def test_long_rows(cuda_device, dtype, V):
+    """Equal weights, 2^15 of them to a lane's sum: with V (24-bit) weights every running sum is a whole
+    multiple of one, exact in 64 bits, so that the token is floor(u V), whatever the weight. A sum that
+    carried its errors in 32 bits over the whole piece drifts by tens of tokens here."""
+    u = torch.tensor([0.25, 0.7311, 0.99999])
+    for weight in (1.37 / V, 1.0 / V, 0.73 / V):
+        p = torch.full((1, 1, V), weight, dtype=dtype, device=cuda_device)
+        for x in u:
+            acc, tok = _lib.verify_drafts(p, torch.empty(1, 0, dtype=torch.int32, device=cuda_device), x.view(1, 1).to(cuda_device))
+            assert acc.tolist() == [0]
+            assert tok.item() == int(np.floor(float(x) * V)), (weight, float(x))
+        del p
