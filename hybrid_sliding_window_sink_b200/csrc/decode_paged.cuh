@@ -29,9 +29,11 @@
 // Precision: bf16 products are exact with fp32 sums. P is carried as two bf16 terms (high part
 // and remainder, 16 significant bits), so that the only visible rounding is that of the output:
 // one bf16 term made the output's error 1.4 times that of the rounding alone. FP8 pages: bytes
-// and Q become f16 (exact for |q| <= 65504), the K scale multiplies the fp32 score, and the V
-// scale joins the weight in its exponent (2^(s + log2|vs| - R) with a running maximum R of its
-// own), so scales of any size keep P inside f16's normal range where it matters.
+// and Q become f16 (exact for 2^-17 <= |q| <= 65504, off by at most 2^-25 below: half of f16's smallest
+// step), the K scale multiplies the fp32 score, and the V scale joins the weight in its exponent
+// (2^(s + log2|vs| - R) with a running maximum R of its own), so normal scales of any size keep P inside
+// f16's normal range where it matters: a weight times its V scale 2^25 and more below the largest of the
+// run drops out of O, not out of the denominator, which sums fp32 weights.
 #pragma once
 
 #include "ptx.cuh"

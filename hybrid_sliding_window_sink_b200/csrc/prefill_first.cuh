@@ -563,15 +563,15 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
       float ref = -INFINITY;                                // reference of P (log2 units)
       float sum0 = 0.f, sum1 = 0.f;                         // of its even and odd columns
       const unsigned long long sc2 = f2_pack(p.scale_log2, p.scale_log2);
-      // One pass over the slot blocks, one block per turn. The reference is the maximum of the first
-      // block that holds a key of the row, rounded up to a whole step, and moves only when a later
-      // block lies 2^8 above it (the P written so far are then scaled by a power of two, so exactly;
-      // rare). P = 2^(a - ref) stays within 2^8 of 1 at its largest, which f16 carries with all its 11
-      // bits. A pass of its own for the maximum cost six TMEM round trips more; two blocks per turn, in
-      // variants for full and partial ones, more code than the instruction caches of an SM that runs
-      // four different roles hold (stalls for instructions doubled). n = 32768, 64/8 heads, one after
-      // the other under the power cap: two passes 553 us, pairs in one pass 573 (cold 515), with their
-      // loads ahead 620, this 461 (cold 411).
+      // One pass over the slot blocks, one block per turn. The reference is the maximum of the first block that
+      // holds a key of the row, rounded up to a whole step, and moves only when a later block lies 2^8 above it
+      // (the P written so far are then scaled by a power of two: exact while they stay normal, else off by at
+      // most 2^-25, as a weight that small is when it is first written; rare). P = 2^(a - ref) stays within 2^8
+      // of 1 at its largest, which f16 carries with all its 11 bits. A pass of its own for the maximum cost six
+      // TMEM round trips more; two blocks per turn, in variants for full and partial ones, more code than the
+      // instruction caches of an SM that runs four different roles hold (stalls for instructions doubled). n =
+      // 32768, 64/8 heads, one after the other under the power cap: two passes 553 us, pairs in one pass 573
+      // (cold 515), with their loads ahead 620, this 461 (cold 411).
       uint32_t v[16];
       int elo, ehi;
       tmem_ld16(trow, v);
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kSwaThreads, 1)
         const float pm = fmaxf(fmax3(ma, x[14], x[15]), mb) * p.scale_log2;
         const bool move = pm > ref + 8.f;                 // (also the first key of the row)
         const float was = ref;
-        ref = move ? ceilf(pm) : ref;                     // whole steps: scaling P is exact
+        ref = move ? ceilf(pm) : ref;                     // whole steps: P is scaled by a power of two
         if (__any_sync(0xffffffffu, move && was != -INFINITY)) {
           const float al = move && was != -INFINITY ? ex2(was - ref) : 1.f;
           sum0 *= al;

@@ -170,6 +170,27 @@ def test_offsets_beyond_32_bits(cuda_device):
     check(out, lse, o, l, mass, 2.0 ** -16, score_error(wl.to_f64(inp["q"]), wl.to_f64(kn), SCALE), "far pages")
 
 
+@pytest.mark.gpu
+def test_agrees_with_the_linear_cache_within_the_roundings(cuda_device):
+    """Both outputs per element: a bf16 rounding each, and P's rounding on the sum of weights times |v|
+    (half a step of bf16 on the linear cache, 2^-16 here), with the score errors of both."""
+    lengths = [3000, 1, 1234]
+    lin = wl.decode_inputs(3, 64, 4, 3000, lengths, seed=14)
+    pad = lambda x: torch.nn.functional.pad(x, (0, 0, 0, 0, 0, 47 * 64 - 3000)).reshape(3 * 47, 64, 4, -1)  # noqa: E731
+    table = torch.arange(3 * 47, dtype=torch.int32).view(3, 47)
+    d = {k: v.to(cuda_device) for k, v in lin.items()}
+    a = _lib.decode(d["q"], d["k_cache"], d["v_cache"], d["lengths"], d["sink"], kind="linear")
+    b = _lib.decode_paged(d["q"], pad(d["k_cache"]), pad(d["v_cache"]), table.to(cuda_device), d["lengths"], d["sink"])
+    torch.cuda.synchronize()
+    o, _, mass, _ = serve.decode_paged(wl.to_f64(lin["q"]), wl.to_f64(pad(lin["k_cache"])), wl.to_f64(pad(lin["v_cache"])),
+                                       table.numpy(), lengths, 0, 0, wl.to_f64(lin["sink"]))
+    delta = score_error(wl.to_f64(lin["q"]), wl.to_f64(lin["k_cache"]), SCALE)
+    # off from the definition before its rounding (2^-18: sums and exponentials, as serve_util.check), each side
+    off = mass * (BF16 + 2 * delta + 2.0 ** -18) + mass * (2.0 ** -16 + 2 * delta + 2.0 ** -18)
+    tol = 2 * np.abs(o) * BF16 + off * (1 + BF16)
+    assert (np.abs(wl.to_f64(a[0]) - wl.to_f64(b[0])) <= tol).all()
+
+
 # ------------------------------------------------------------------ FP8 pages
 def _fp8(inp, spread=0.0, seed=0):
     k8, ks = wl.fp8_cache(inp["k"])
@@ -229,6 +250,28 @@ def test_fp8_strided_and_split(cuda_device):
     for name in ("k", "v", "ks", "vs"):
         assert f[name].stride(0) // (f[name][0, 0].numel()) == 32
     _check_fp8(f, cuda_device, what="fp8 strided")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("small", [2.0 ** -6, 2.0 ** -12, 2.0 ** -16])
+def test_fp8_small_queries_and_large_key_scales(cuda_device, small):
+    """Q becomes f16: exact while 2^-17 <= |q| <= 65504, off by at most 2^-25 an element below (half of
+    f16's smallest step), which large K scales bring back into the scores."""
+    inp = _fp8(paged_inputs([333, 40], 16, 2, 16, seed=24))
+    inp["q"] = (inp["q"].float() * small).bfloat16()
+    inp["ks"] = inp["ks"] / small
+    k = ref.dequant_fp8(inp["k"].numpy(), inp["ks"].numpy())
+    v = ref.dequant_fp8(inp["v"].numpy(), inp["vs"].numpy())
+    d = to_dev(inp, cuda_device)
+    out, lse = _lib.decode_paged_fp8(d["q"], d["k"], d["v"], d["ks"], d["vs"], d["table"], d["lengths"], d["sink"])
+    torch.cuda.synchronize()
+    o, l, mass, top = _oracle(inp, 0, 0, True, k, v)
+    # a score is off by 2^-25 for each of the 192 dims times |k| of that dim, besides the sum's own error;
+    # two scores off by delta move a weight by a factor of at most e^(2 delta)
+    conv = SCALE * 2.0 ** -25 * np.abs(k).sum(-1).max()
+    delta = 2 * score_error(wl.to_f64(inp["q"]), k, SCALE) + conv
+    check(out, lse, o, l, mass, F16 + 2.0 ** -18 + (np.expm1(2 * delta) - 2 * delta), delta, f"small {small}",
+          (333 * 2.0 ** -25 * top * 2)[..., None])
 
 
 # ------------------------------------------------------------------ cache writes
