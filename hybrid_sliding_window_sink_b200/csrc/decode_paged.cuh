@@ -166,10 +166,7 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<FP8>::CTAS) decode_paged_
   const int cta = blockIdx.x;
   const long long U = static_cast<long long>(p.B) * p.Hkv;
   const bool by_unit = U <= p.nctas;          // headers by unit, else by CTA
-  if (cta >= N) {
-    if (!by_unit && tid == 0 && p.hdr) p.hdr[cta] = make_int4(0, -1, -1, 0);
-    return;
-  }
+  if (cta >= N) return;                       // (only while N = T < nctas, and U <= T: headers are by unit)
   // tile T c / N as c (T div N) + c (T mod N) div N
   const long long quo = div_ll(T, N);
   const int rem = static_cast<int>(T - quo * N);
