@@ -520,8 +520,8 @@ def _cuda_device(t, name):
 def prefill_first(q, k, v, sink=None, *, window, n_first, pos_offset=0, k_prefix_rotated=True, rope_theta=1e4,
                   rot_dims=64, softmax_scale=0.0, out=None, lse=None, want_lse=True, stream=None):
     """mimo_attn_prefill_first. q [B,n,Hq,192] at positions pos_offset on; k, v [B,pos_offset+n,Hkv,·]
-    (prefix K rotated when k_prefix_rotated). A query sees its last ``window`` tokens and the first
-    ``n_first``. Returns (out [B,n,Hq,128] bf16, lse [B,Hq,n] fp32 or None)."""
+    (prefix K rotated when k_prefix_rotated). A query sees its last ``window`` tokens and, before
+    them, those of the first ``n_first`` (window <= 0: everything up to it). Returns (out [B,n,Hq,128] bf16, lse [B,Hq,n] fp32 or None)."""
     if out is None and lse is None and stream is None and (call := _usual()):
         got = call.prefill_first(q, k, v, sink, window, n_first, pos_offset, k_prefix_rotated, rope_theta, rot_dims,
                                  softmax_scale, want_lse)

@@ -1,7 +1,7 @@
 // prefill_first.cuh - sm_100a prefill of an SWA layer with window W <= 129, 8 query heads per KV head,
 // and the first n_first <= 16 tokens kept visible behind the window.
 //
-// Row i sees J_i = [max(0, i - W + 1), i] and [0, n_first); the rest of the math, the row blocks, the
+// Row i sees J_i = [lo, i] and [0, min(n_first, lo)), lo = max(0, i - W + 1); the rest of the math, the row blocks, the
 // K/V ring, the roles and the precision are those of prefill_swa.cuh (its ring, chunked prefill and
 // waits are described there). What differs:
 //   * The first tokens sit in one more unit behind the ring, loaded once per (sequence, KV head) run:

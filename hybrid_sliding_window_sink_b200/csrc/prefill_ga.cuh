@@ -22,7 +22,9 @@
 // WIN: a window (any width) with the first n_first tokens kept visible. An item's tiles are then
 // the 128-key tiles of the first tokens that lie before its window, followed by those from the
 // one holding the lowest key of its window on; only tiles that some row masks in part pay for
-// masks, and for a look at their V rows (see v_row_not_finite).
+// masks, and for a look at their V rows (see v_row_not_finite). P stays one bf16 term, as without a window:
+// the output's error against 64 bits is 1.35 times that of its bf16 rounding (wide window, n = 8192: 2.20e-3
+// and 1.67e-3); a second term, as the paged decode has, would double the products of P V.
 // Lazy rescaling: a row keeps its reference max until a tile raises it by more than 8 (log2
 // units); P = 2^(a - ref) then stays below 2^8, and O / l are rescaled only when the
 // reference moves.

@@ -39,8 +39,15 @@
  *    to f16 without clamping (a larger |q| becomes infinite). A build compiled with
  *    MIMO_DEBUG records every such value in the device error word (bit 16, see
  *    mimo_attn_last_device_error). Outputs are rounded to bf16, lse is fp32.
- *  - The paged decode carries P with 16 significant bits on bf16 pages and 11 on FP8 pages; its FP8
- *    form multiplies Q in f16 as the FP8 decode does.
+ *  - P, the softmax weights: one bf16 term (8 significant bits) in the prefill kernels other than the SWA
+ *    ring kernels (f16, 11 bits) - the output's error is then about 1.35 times that of its rounding to
+ *    bf16 alone. The paged decode carries P with 16 significant bits on bf16 pages; on FP8 pages with 11,
+ *    and a weight times its V scale below 2^-25 of the largest counts as 0 in the output (not in its
+ *    denominator).
+ *  - Where Q, K or V become f16, values below 2^-17 are off by up to 2^-25 (2^-24 is f16's smallest step).
+ *    The FP8 form of the paged decode multiplies Q in f16 as the FP8 decode does. E4M3 rows written by
+ *    mimo_attn_cache_append_paged_fp8 come from x / scale good to 2^-22, so a value that close to the
+ *    middle of two E4M3 numbers may become either.
  *  - Thread safety: calls may be made from several host threads; the shared mutable
  *    state is the device error word read by mimo_attn_last_device_error and the scratch
  *    array of mimo_attn_sparse_noalloc (see there).
@@ -308,15 +315,15 @@ size_t mimo_attn_select_workspace_size(const mimo_shape* shape, int cache_capaci
 /*
  * Prefill with a sliding window and pinned first tokens: as mimo_attn_prefill_chunk (whole
  * sequences with pos_offset = 0), but the query at position i sees
- *   J_i = [max(0, i - window + 1), i] and [0, n_first)
- * (a token in both counts once). n_first >= 0, any size; n_first = 0 or window <= 0 is
- * mimo_attn_prefill_chunk itself. Positions stay absolute: a first token keeps its own rotation.
- * Errors as mimo_attn_prefill_chunk, MIMO_ERR_SHAPE also for n_first < 0.
+ *   J_i = [lo, i] and [0, min(n_first, lo)), lo = max(0, i - window + 1):
+ * its window, and those of the first tokens that lie before it. n_first >= 0, any size; n_first = 0 or
+ * window <= 0 is mimo_attn_prefill_chunk itself. Positions stay absolute: a first token keeps its own
+ * rotation. Errors as mimo_attn_prefill_chunk, MIMO_ERR_SHAPE also for n_first < 0.
  * The decode of such a layer is mimo_attn_decode_paged with the same window and n_first.
  * With window > 0 and n_first > 0, a V row that is not finite does not reach queries that mask its key
  * (behind them in a padded batch, say). A query that sees it is not finite in the columns of V's NaN and
- * infinities; where some query of the same tile masks the key (everywhere with window <= 129, 8 heads per KV
- * head) all its 128 columns and its lse become NaN, although lse does not depend on V.
+ * infinities; where other queries of its tile mask the key, all its 128 columns and its lse may be NaN,
+ * although lse does not depend on V.
  */
 mimo_status mimo_attn_prefill_first(const mimo_shape* shape, const void* q, const void* k, const void* v,
                                     int pos_offset, int k_prefix_rotated, const float* sink, int window,
