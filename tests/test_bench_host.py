@@ -160,3 +160,11 @@ def test_bench_line_fits_the_driver_tail():
                                              "ga_decode", "sparse_decode")}}}
     text = json.dumps(line, separators=(",", ":"))
     assert len(text) < 2600, len(text)
+
+
+def test_recorded_traffic_is_of_the_present_sources():
+    """A record is reported only while its kernel's sources are those of the capture: a change to one of
+    them (to a header that several kernels share, too) goes with new captures."""
+    with open(os.path.join(bench.ROOT, "profiles", "traffic.json")) as f:
+        keys = [k for k in json.load(f) if not k.startswith("_")]
+    assert keys and [k for k in keys if bench.traffic_for(k, 1000) is None] == []
