@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int khi = FIRST && j < nft ? lo - 1 : pos;   // last key this tile may contribute
         // (FIRST) the keys below the window that are no first tokens, [n_first, klo), as one comparison (two:
         // 2902 us in the case above, this 2774)
-        const unsigned band = FIRST ? static_cast<unsigned>(max(0, klo - first_of(p))) : 0u;
+        const unsigned band = FIRST && klo > first_of(p) ? static_cast<unsigned>(klo - first_of(p)) : 0u;
         auto key_ok = [&](int key) -> bool {
           if constexpr (FIRST) return static_cast<unsigned>(key - first_of(p)) >= band && key <= khi;
           return key >= klo && key <= khi;
